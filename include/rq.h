@@ -71,6 +71,10 @@ typedef enum { RQ_BF16 = 0, RQ_FP16 = 1 } rq_dtype;
 #define RQ_MAX_HIDDEN 262144
 #define RQ_QK_HEAD_DIM 128
 #define RQ_QK_MAX_HEADS 65536
+#define RQ_KV_MAX_PAGE 65536
+#define RQ_ATTN_MAX_KEYS 1073741824
+#define RQ_ATTN_MAX_TOKENS 16777216
+#define RQ_ATTN_MAX_SEQS 1048576
 
 /*
  * Residual add + RMSNorm + per-tensor FP8 E4M3.
@@ -379,6 +383,125 @@ rq_status rq_add_rmsnorm_nvfp4_dynamic_swizzled(
     const void *weight, float eps, float *d_global_scale_out,
     uint8_t *q_packed, uint8_t *block_scales, void *norm_out, int64_t rows,
     int64_t hidden, rq_dtype dt, rq_stream_t stream);
+
+/*
+ * ---- Paged KV cache held in NVFP4.
+ * kv_pool is [num_pages, n_kv_heads, page_size * 144] bytes, page_size a
+ * multiple of 16 (at most RQ_KV_MAX_PAGE).  A page holds, for each head,
+ * page_size / 16 groups of 16 tokens, 2304 bytes each:
+ *   K codes [16][64] | V codes [16][64] | K scales [16][8] | V scales [16][8]
+ * (64 bytes: the 128 E2M1 codes of a head row, even element in the low
+ * nibble; 8 bytes: one E4M3 scale per 16 elements).  The value of an element
+ * is e2m1(code) * e4m3(scale) / gs, with gs the fp32 global scale of K or V in
+ * the quantising direction (e.g. 2688 / amax, rq_nvfp4_global_scale_from_amax).
+ * Limits: num_pages * page_size <= 2^35, num_pages * page_size / 16 *
+ * n_kv_heads < 2^31.
+ *
+ * Appends the keys and values of n_tokens tokens and writes the queries:
+ *   n = x * rstd * w over each head row of Q and K, rstd = 1 / sqrt(mean x^2 +
+ *   eps); a NULL weight leaves that side without the norm (n = x);
+ *   o_i = n_i c_i - n_{i+64} s_i, o_{i+64} = n_{i+64} c_i + n_i s_i (NeoX) with
+ *   the cos / sin row of the token's position;
+ *   Q: q_out = dt(o);  K: NVFP4(o), V: NVFP4(v) into the token's slot, where
+ *   sf = E4M3(gs a / 6), a = max |y| of the block, code = E2M1(y gs / sf)
+ *   (codes of signed zeros where sf = 0).
+ * Unlike the calls above there is no intermediate rounding: q_out is fp32
+ * arithmetic rounded once, and the codes are those of the real-valued formula
+ * (decided in double precision wherever fp32 leaves a code open), so the bytes
+ * of the cache do not depend on any order of summation.
+ * Source: "perf: add fused norm + RoPE + uniform fp8 store for TRT-LLM DSv4
+ * sparse attention" (SGLang PR 32975), review thread, for the norm + RoPE +
+ * cache store; "Add AutoDeploy NVFP4 RMSNorm quant fusion" (TensorRT-LLM PR
+ * 14361) for the NVFP4 format.  The cache layout is this library's.
+ *
+ *   q, k, v          token t, head h at base + t*stride + h*head_dim elements
+ *                    (strides multiples of 8, >= heads * head_dim)
+ *   q_weight, k_weight [head_dim] dt or NULL
+ *   positions, cos_sin_cache, max_pos  as in rq_qk_rmsnorm_rope_fp8
+ *   q_out            [n_tokens, n_q_heads, head_dim] dt
+ *   slots            [n_tokens] int64 (8-byte aligned): page * page_size + index in the page;
+ *                    a slot outside the cache stores nothing for that token
+ *                    (its q_out is written).  Of two tokens with one slot,
+ *                    which one's bytes stay is unspecified.
+ *   n_q_heads or n_kv_heads may be 0 (that side's pointers may be NULL).
+ */
+rq_status rq_qkv_rope_nvfp4_kv_append(
+    const void *q, const void *k, const void *v, int64_t q_token_stride,
+    int64_t k_token_stride, int64_t v_token_stride, int64_t n_tokens,
+    int n_q_heads, int n_kv_heads, int head_dim, const void *q_weight,
+    const void *k_weight, float eps, const int32_t *positions,
+    const float *cos_sin_cache, int64_t max_pos, const float *d_k_global_scale,
+    const float *d_v_global_scale, void *q_out, uint8_t *kv_pool,
+    int64_t num_pages, int page_size, const int64_t *slots, rq_dtype dt,
+    rq_stream_t stream);
+
+/*
+ * Attention over that cache.  Query i of sequence b, of q_len_b, stands at
+ * position p = kv_len_b - q_len_b + i and sees the keys j with j <= p and,
+ * with window > 0, j > p - window:
+ *   s_j = sm_scale * (q . k_j),  out = sum_j softmax(s)_j v_j,
+ *   lse = ln sum_j exp s_j.
+ * A query that sees no key (an empty sequence, p < 0, unreadable pages) gets
+ * out = 0 and lse = -inf.  n_q_heads is a multiple of n_kv_heads; query head h
+ * reads KV head h / (n_q_heads / n_kv_heads).
+ * Numerics: cached values are exact in the products (an E2M1 code times its
+ * E4M3 scale is an fp16 value); sums, maxima and exponentials are fp32; the
+ * probabilities enter the product with V as fp16; out is rounded once.  bf16
+ * queries enter as fp16 after a power-of-two scaling of the row (exact but for
+ * elements below 2^-14 of the row's largest, whose error is 2^-25 of it).
+ *
+ *   q               token t at q + t*q_token_stride (heads contiguous)
+ *   block_table     sequence b's page ids: block_table[b*table_stride + j] is
+ *                   the page of tokens j*page_size ...; a page id outside [0,
+ *                   num_pages) hides its tokens.  Entries past the sequence's
+ *                   last page are not read.
+ *   kv_lens         [n_seqs] int32 keys of each sequence, the new tokens among
+ *                   them; clamped to [0, pages_per_seq * page_size].  Cache
+ *                   bytes of later tokens may hold anything; scale bytes of
+ *                   the tokens themselves are finite E4M3 values (the append
+ *                   writes no others).
+ *   out             [n_tokens, n_q_heads, head_dim] dt
+ *   lse             [n_tokens, n_q_heads] fp32, or NULL
+ *   workspace       rq_paged_attn_nvfp4_workspace_bytes() bytes, 16-byte
+ *                   aligned, contents of no meaning before or after.  It is in
+ *                   use until the call's work on the stream is done: calls (or
+ *                   captured graphs) that may run at the same time need one
+ *                   each.  A smaller one returns RQ_ERR_SHAPE.
+ *   sm_scale > 0; window >= 0 (0: none); pages_per_seq * page_size <=
+ *   RQ_ATTN_MAX_KEYS, n_tokens <= RQ_ATTN_MAX_TOKENS, n_tokens * n_q_heads <
+ *   2^31, n_seqs <= RQ_ATTN_MAX_SEQS.
+ *
+ * rq_paged_decode_attn_nvfp4: one query per sequence (n_tokens = n_seqs).
+ * rq_paged_extend_attn_nvfp4: sequence b's queries are the rows q_starts[b] ..
+ *   q_starts[b+1] - 1 of q ([n_seqs + 1] int32, non-decreasing; clamped to
+ *   [0, n_tokens]); rows of out outside every sequence are left as they are.
+ *   max_q_len is the caller's bound on the query lengths: it chooses kernels
+ *   and grids, and does not change what is computed.
+ * Source: the attention that the pages' fused Q/K store feeds ("perf: add
+ * fused norm + RoPE + uniform fp8 store for TRT-LLM DSv4 sparse attention"),
+ * over the NVFP4 cache above; standard softmax attention.
+ */
+rq_status rq_paged_decode_attn_nvfp4(
+    const void *q, int64_t q_token_stride, int64_t n_seqs, int n_q_heads,
+    int n_kv_heads, int head_dim, const uint8_t *kv_pool, int64_t num_pages,
+    int page_size, const int32_t *block_table, int64_t table_stride,
+    int64_t pages_per_seq, const int32_t *kv_lens, float sm_scale, int window,
+    const float *d_k_global_scale, const float *d_v_global_scale, void *out,
+    float *lse, void *workspace, size_t workspace_bytes, rq_dtype dt,
+    rq_stream_t stream);
+rq_status rq_paged_extend_attn_nvfp4(
+    const void *q, int64_t q_token_stride, int64_t n_tokens,
+    const int32_t *q_starts, int64_t n_seqs, int64_t max_q_len, int n_q_heads,
+    int n_kv_heads, int head_dim, const uint8_t *kv_pool, int64_t num_pages,
+    int page_size, const int32_t *block_table, int64_t table_stride,
+    int64_t pages_per_seq, const int32_t *kv_lens, float sm_scale, int window,
+    const float *d_k_global_scale, const float *d_v_global_scale, void *out,
+    float *lse, void *workspace, size_t workspace_bytes, rq_dtype dt,
+    rq_stream_t stream);
+/* Workspace of either attention call. */
+size_t rq_paged_attn_nvfp4_workspace_bytes(int n_q_heads, int n_kv_heads);
+/* Bytes of one page of one head: page_size * 144 (0 for an invalid size). */
+size_t rq_nvfp4_kv_page_bytes(int page_size);
 
 /* Output sizes of the NVFP4 call (the linear, unswizzled layout):
  * rows * hidden / 2 packed bytes and rows * hidden / 16 scale bytes.

@@ -1,6 +1,7 @@
 """nvfp4_quant_gb300: Python binding of librq, the GB300 (sm_103a) library of
-fused residual add + RMSNorm + FP8 / NVFP4 quantisation kernels and the
-per-head Q/K RMSNorm + RoPE + FP8 store.
+fused residual add + RMSNorm + FP8 / NVFP4 quantisation kernels, the per-head
+Q/K RMSNorm + RoPE + FP8 store, and the paged NVFP4 KV cache: its append and
+the attention that reads it.
 
 This module only marshals arguments: it turns torch CUDA tensors into device
 pointers and sizes, calls the C ABI (include/rq.h) through ctypes, and raises
@@ -20,11 +21,16 @@ RQ_BF16, RQ_FP16 = 0, 1
 RQ_MAX_HIDDEN = 262144
 RQ_QK_HEAD_DIM = 128
 RQ_QK_MAX_HEADS = 65536
+RQ_KV_MAX_PAGE = 65536
+RQ_ATTN_MAX_KEYS = 1073741824
+RQ_ATTN_MAX_TOKENS = 16777216
+RQ_ATTN_MAX_SEQS = 1048576
 STATUS = {0: "RQ_OK", 1: "RQ_ERR_NULL", 2: "RQ_ERR_SHAPE", 3: "RQ_ERR_DTYPE",
           4: "RQ_ERR_MISALIGNED", 5: "RQ_ERR_ALIAS", 6: "RQ_ERR_UNSUPPORTED", 7: "RQ_ERR_CUDA"}
 
 # exported symbol -> (restype, argtypes)
 _vp, _i64, _f32, _int = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int
+_size = ctypes.c_size_t
 SIGNATURES = {
     "rq_add_rmsnorm_fp8": (_int, [_vp, _vp, _vp, _vp, _f32, _vp, _vp, _vp, _i64, _i64, _int, _vp]),
     "rq_add_rmsnorm_nvfp4": (_int, [_vp, _vp, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _i64, _i64,
@@ -62,6 +68,17 @@ SIGNATURES = {
                                       _vp]),
     "rq_gated_rmsnorm_nvfp4_swizzled": (_int, [_vp, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _i64, _i64,
                                                _int, _vp]),
+    "rq_qkv_rope_nvfp4_kv_append": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _int, _int,
+                                           _vp, _vp, _f32, _vp, _vp, _i64, _vp, _vp, _vp, _vp,
+                                           _i64, _int, _vp, _int, _vp]),
+    "rq_paged_decode_attn_nvfp4": (_int, [_vp, _i64, _i64, _int, _int, _int, _vp, _i64, _int, _vp,
+                                          _i64, _i64, _vp, _f32, _int, _vp, _vp, _vp, _vp, _vp,
+                                          _size, _int, _vp]),
+    "rq_paged_extend_attn_nvfp4": (_int, [_vp, _i64, _i64, _vp, _i64, _i64, _int, _int, _int, _vp,
+                                          _i64, _int, _vp, _i64, _i64, _vp, _f32, _int, _vp, _vp,
+                                          _vp, _vp, _vp, _size, _int, _vp]),
+    "rq_paged_attn_nvfp4_workspace_bytes": (_size, [_int, _int]),
+    "rq_nvfp4_kv_page_bytes": (_size, [_int]),
     "rq_status_string": (ctypes.c_char_p, [_int]),
     "rq_last_error": (ctypes.c_char_p, []),
     "rq_version": (_int, []),
@@ -417,6 +434,157 @@ def rq_qk_rmsnorm_rope_fp8_dynamic(q, k, q_weight, k_weight, eps, positions, cos
         _stream(stream)))
 
 
+# ------------------------------------------------------- paged NVFP4 KV cache
+def _same_device(ref, *others):
+    """The index of the device that every given tensor lies on."""
+    if not ref.is_cuda:
+        raise ValueError("every tensor argument must be a CUDA tensor (got one on %s)" % ref.device)
+    dev = ref.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError("every tensor argument must lie on %s (got one on %s)" % (dev, t.device))
+    return dev.index
+
+
+def _call_on(dev, fn, args, stream):
+    """fn(*args, stream) with the tensors' device current; stream None is that
+    device's current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    stream = getattr(stream, "cuda_stream", stream)
+    if torch.cuda.current_device() == dev:
+        _check(fn(*args, stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, stream))
+
+
+def _typed(t, dtype, numel, name):
+    """A contiguous tensor of at least numel elements of a type."""
+    if t is None or t.dtype != dtype or not t.is_contiguous() or t.numel() < numel:
+        raise ValueError("%s must be a contiguous %s tensor of at least %d elements"
+                         % (name, str(dtype).replace("torch.", ""), numel))
+    return t.data_ptr()
+
+
+def _cache(kv_pool, page_size, heads):
+    if kv_pool.dtype != torch.uint8 or kv_pool.dim() != 3 or not kv_pool.is_contiguous() or \
+            kv_pool.shape[1] != heads or kv_pool.shape[2] != page_size * 144:
+        raise ValueError("kv_pool must be a contiguous uint8 [num_pages, n_kv_heads, page_size * 144] "
+                         "tensor with %d heads" % heads)
+    return kv_pool.data_ptr(), kv_pool.shape[0], int(page_size)
+
+
+def _head_rows(t, name, like=None):
+    if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+        raise ValueError("%s must be a [tokens, heads, head_dim] view with contiguous heads" % name)
+    if like is not None and (t.shape[0] != like.shape[0] or t.dtype != like.dtype
+                             or t.shape[2] != like.shape[2]):
+        raise ValueError("%s must match q in token count, head_dim and dtype" % name)
+    # a single token's stride says nothing (torch leaves any value there)
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def rq_qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos_sin_cache,
+                                k_global_scale, v_global_scale, q_out, kv_pool, slots, page_size,
+                                stream=None):
+    """Append K and V to a paged NVFP4 cache with the per-head norm (a None
+    weight: no norm) and RoPE on the way, and write the rotated queries
+    (include/rq.h).  q [T, Hq, 128], k, v [T, Hk, 128] may be token-strided
+    views; q_out [T, Hq, 128]; kv_pool uint8 [pages, Hk, page_size * 144];
+    slots int64 [T] (page * page_size + index; outside the cache: not stored)."""
+    dev = _same_device(q, k, v, q_weight, k_weight, positions, cos_sin_cache, k_global_scale,
+                       v_global_scale, q_out, kv_pool, slots)
+    qp, qs = _head_rows(q, "q")
+    kp, ks = _head_rows(k, "k", q)
+    vp, vs = _head_rows(v, "v", q)
+    t, hq, d = q.shape
+    hk = k.shape[1]
+    if v.shape[1] != hk:
+        raise ValueError("k and v must have the same heads")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != q.dtype or w.numel() != d or not w.is_contiguous()):
+            raise ValueError("weights must be [head_dim] of q's dtype")
+    if cos_sin_cache.dtype != torch.float32 or cos_sin_cache.dim() != 2 or \
+            cos_sin_cache.shape[1] != d or not cos_sin_cache.is_contiguous():
+        raise ValueError("cos_sin_cache must be a contiguous [max_pos, %d] float32 tensor" % d)
+    if q_out.dtype != q.dtype:
+        raise ValueError("q_out must have q's dtype")
+    pool, pages, page = _cache(kv_pool, page_size, hk)
+    _call_on(dev, lib().rq_qkv_rope_nvfp4_kv_append, (
+        qp, kp, vp, qs, ks, vs, t, hq, hk, d, None if q_weight is None else q_weight.data_ptr(),
+        None if k_weight is None else k_weight.data_ptr(), float(eps),
+        _typed(positions, torch.int32, t, "positions"), cos_sin_cache.data_ptr(),
+        cos_sin_cache.shape[0], _typed(k_global_scale, torch.float32, 1, "k_global_scale"),
+        _typed(v_global_scale, torch.float32, 1, "v_global_scale"),
+        _typed(q_out, q.dtype, t * hq * d, "q_out"), pool, pages, page,
+        _typed(slots, torch.int64, t, "slots"), _dt(q)), stream)
+
+
+def _paged_attn(q, kv_pool, page_size, block_table, q_starts, max_q_len, kv_lens, k_gs, v_gs,
+                sm_scale, out, workspace, window, lse, stream):
+    dev = _same_device(q, kv_pool, block_table, q_starts, kv_lens, k_gs, v_gs, out, workspace, lse)
+    qp, qs = _head_rows(q, "q")
+    t, hq, d = q.shape
+    if kv_pool.dim() != 3 or kv_pool.shape[1] < 1 or hq % kv_pool.shape[1] != 0:
+        raise ValueError("q's heads must be a multiple of the cache's")
+    hk = kv_pool.shape[1]
+    pool, pages, page = _cache(kv_pool, page_size, hk)
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
+            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be an int32 [n_seqs, pages_per_seq] tensor with contiguous rows")
+    n, per = block_table.shape
+    row = block_table.stride(0) if n > 1 else per
+    tail = (_typed(kv_lens, torch.int32, n, "kv_lens"), float(sm_scale), int(window),
+            _typed(k_gs, torch.float32, 1, "k_global_scale"),
+            _typed(v_gs, torch.float32, 1, "v_global_scale"), _typed(out, q.dtype, t * hq * d, "out"),
+            None if lse is None else _typed(lse, torch.float32, t * hq, "lse"), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), _dt(q))
+    L = lib()
+    if q_starts is None:
+        if t != n:
+            raise ValueError("q must hold one query per sequence")
+        _call_on(dev, L.rq_paged_decode_attn_nvfp4, (
+            qp, qs, n, hq, hk, d, pool, pages, page, block_table.data_ptr(), row, per) + tail, stream)
+    else:
+        _call_on(dev, L.rq_paged_extend_attn_nvfp4, (
+            qp, qs, t, _typed(q_starts, torch.int32, n + 1, "q_starts"), n, int(max_q_len), hq, hk, d,
+            pool, pages, page, block_table.data_ptr(), row, per) + tail, stream)
+
+
+def rq_paged_decode_attn_nvfp4(q, kv_pool, page_size, block_table, kv_lens, k_global_scale,
+                               v_global_scale, sm_scale, out, workspace, window=0, lse=None,
+                               stream=None):
+    """Attention of one query per sequence over a paged NVFP4 cache
+    (include/rq.h).  q, out [n_seqs, Hq, 128]; block_table int32 [n_seqs,
+    pages_per_seq]; kv_lens int32 [n_seqs]; lse float32 [n_seqs, Hq] or None;
+    workspace: rq_paged_attn_nvfp4_workspace_bytes(Hq, Hk) bytes, not shared by
+    calls that may run at the same time."""
+    _paged_attn(q, kv_pool, page_size, block_table, None, 1, kv_lens, k_global_scale,
+                v_global_scale, sm_scale, out, workspace, window, lse, stream)
+
+
+def rq_paged_extend_attn_nvfp4(q, kv_pool, page_size, block_table, q_starts, kv_lens, max_q_len,
+                               k_global_scale, v_global_scale, sm_scale, out, workspace, window=0,
+                               lse=None, stream=None):
+    """Causal attention of each sequence's last queries over a paged NVFP4
+    cache (include/rq.h).  q, out [tokens, Hq, 128], sequence b's rows
+    q_starts[b] .. q_starts[b + 1] - 1 (int32 [n_seqs + 1]); kv_lens counts the
+    new tokens too; max_q_len: the longest run of queries (a bound)."""
+    if q_starts is None:
+        raise ValueError("q_starts must be an int32 [n_seqs + 1] tensor")
+    _paged_attn(q, kv_pool, page_size, block_table, q_starts, max_q_len, kv_lens, k_global_scale,
+                v_global_scale, sm_scale, out, workspace, window, lse, stream)
+
+
+def rq_paged_attn_nvfp4_workspace_bytes(n_q_heads, n_kv_heads):
+    return int(lib().rq_paged_attn_nvfp4_workspace_bytes(n_q_heads, n_kv_heads))
+
+
+def rq_nvfp4_kv_page_bytes(page_size):
+    return int(lib().rq_nvfp4_kv_page_bytes(page_size))
+
+
 def rq_nvfp4_packed_bytes(rows, hidden):
     return int(lib().rq_nvfp4_packed_bytes(rows, hidden))
 
@@ -489,3 +657,79 @@ def add_rmsnorm_fp8(x, residual, weight, eps, scale, with_norm_out=False, in_pla
     y = torch.empty_like(x) if with_norm_out else None
     rq_add_rmsnorm_fp8(x, residual, res_out, weight, eps, scale, q, y, stream)
     return res_out, q, y
+
+
+class _on_stream:
+    """Allocations inside come from `stream`'s pool, so that a buffer's memory
+    is not handed out again while that stream still uses it.  None: the current
+    stream of the device, nothing to do."""
+
+    def __init__(self, stream, device):
+        if stream is None:
+            self.guard = None
+        else:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(stream, device=device)
+            self.guard = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *e):
+        if self.guard is not None:
+            self.guard.__exit__(*e)
+
+
+def nvfp4_kv_pool(num_pages, n_kv_heads, page_size, device="cuda"):
+    """An empty paged NVFP4 KV cache: zeroed uint8 [pages, heads, page_size * 144]."""
+    nbytes = rq_nvfp4_kv_page_bytes(page_size)
+    if nbytes == 0:
+        raise ValueError("page_size must be a positive multiple of 16, at most %d" % RQ_KV_MAX_PAGE)
+    return torch.zeros((num_pages, n_kv_heads, nbytes), dtype=torch.uint8, device=device)
+
+
+def qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos_sin_cache,
+                             k_global_scale, v_global_scale, kv_pool, slots, page_size, stream=None):
+    """Allocate q_out (torch) and run rq_qkv_rope_nvfp4_kv_append.  Returns
+    q_out [T, Hq, 128]."""
+    with _on_stream(stream, q.device):
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    rq_qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos_sin_cache,
+                                k_global_scale, v_global_scale, q_out, kv_pool, slots, page_size,
+                                stream)
+    return q_out
+
+
+def _attn_buffers(q, kv_pool, with_lse, workspace, stream):
+    with _on_stream(stream, q.device):
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if with_lse else None
+        if workspace is None:
+            workspace = torch.empty((rq_paged_attn_nvfp4_workspace_bytes(q.shape[1], kv_pool.shape[1]),),
+                                    dtype=torch.uint8, device=q.device)
+    return out, lse, workspace
+
+
+def paged_decode_attn_nvfp4(q, kv_pool, page_size, block_table, kv_lens, k_global_scale,
+                            v_global_scale, sm_scale, window=0, with_lse=False, workspace=None,
+                            stream=None):
+    """Allocate the outputs (and, unless given, the workspace) and run
+    rq_paged_decode_attn_nvfp4.  Returns (out, lse or None)."""
+    out, lse, workspace = _attn_buffers(q, kv_pool, with_lse, workspace, stream)
+    rq_paged_decode_attn_nvfp4(q, kv_pool, page_size, block_table, kv_lens, k_global_scale,
+                               v_global_scale, sm_scale, out, workspace, window, lse, stream)
+    return out, lse
+
+
+def paged_extend_attn_nvfp4(q, kv_pool, page_size, block_table, q_starts, kv_lens, max_q_len,
+                            k_global_scale, v_global_scale, sm_scale, window=0, with_lse=False,
+                            workspace=None, stream=None):
+    """Allocate the outputs (and, unless given, the workspace) and run
+    rq_paged_extend_attn_nvfp4.  Returns (out, lse or None); rows of out behind
+    the last sequence are not written."""
+    out, lse, workspace = _attn_buffers(q, kv_pool, with_lse, workspace, stream)
+    rq_paged_extend_attn_nvfp4(q, kv_pool, page_size, block_table, q_starts, kv_lens, max_q_len,
+                               k_global_scale, v_global_scale, sm_scale, out, workspace, window, lse,
+                               stream)
+    return out, lse

@@ -491,6 +491,93 @@ rq_status qk_call(const void *q, const void *k, int64_t q_token_stride, int64_t 
     return cuda_status(e);
 }
 
+// A paged NVFP4 cache of at most 2^35 tokens (so that a token's group is an
+// int) and 2^31 groups over all heads.
+bool valid_pool(int64_t num_pages, int page_size, int heads)
+{
+    if (page_size <= 0 || page_size % 16 != 0 || page_size > RQ_KV_MAX_PAGE) return false;
+    if (num_pages < 0 || num_pages > ((int64_t)1 << 35) / page_size) return false;
+    return num_pages * (page_size / 16) * heads < (int64_t)1 << 31;
+}
+
+int64_t pool_bytes(int64_t num_pages, int page_size, int heads)
+{
+    return num_pages * heads * (page_size / 16) * rq::kKVGroupBytes;
+}
+
+// Argument checks of the attention calls, then the launch.
+rq_status attn_call(const void *q, int64_t q_token_stride, int64_t n_tokens, const int32_t *q_starts,
+                    int64_t n_seqs, int64_t max_q_len, int n_q_heads, int n_kv_heads, int head_dim,
+                    const uint8_t *kv_pool, int64_t num_pages, int page_size,
+                    const int32_t *block_table, int64_t table_stride, int64_t pages_per_seq,
+                    const int32_t *kv_lens, float sm_scale, int window, const float *d_k_gs,
+                    const float *d_v_gs, void *out, float *lse, void *workspace,
+                    size_t workspace_bytes, rq_dtype dt, rq_stream_t stream, bool extend)
+{
+    if (dt != RQ_BF16 && dt != RQ_FP16) return RQ_ERR_DTYPE;
+    if (n_tokens < 0 || n_tokens > RQ_ATTN_MAX_TOKENS || n_seqs < 0 || n_seqs > RQ_ATTN_MAX_SEQS ||
+        max_q_len < 0 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads > RQ_QK_MAX_HEADS ||
+        n_q_heads % n_kv_heads != 0 || n_tokens * n_q_heads >= (int64_t)1 << 31 || window < 0 || !(sm_scale > 0.0f))
+        return RQ_ERR_SHAPE;
+    if (head_dim != RQ_QK_HEAD_DIM) return RQ_ERR_UNSUPPORTED;
+    if (!valid_pool(num_pages, page_size, n_kv_heads) || pages_per_seq < 0 ||
+        table_stride < pages_per_seq || table_stride > (int64_t)1 << 31 ||
+        pages_per_seq > RQ_ATTN_MAX_KEYS / page_size)
+        return RQ_ERR_SHAPE;
+    if (n_tokens == 0 || n_seqs == 0) return RQ_OK;
+    if (q_token_stride % 8 != 0) return RQ_ERR_MISALIGNED;
+    if (q_token_stride < (int64_t)n_q_heads * head_dim || q_token_stride > (int64_t)1 << 40)
+        return RQ_ERR_SHAPE;
+    if (!q || !out || !kv_lens || !d_k_gs || !d_v_gs || !workspace || (extend && !q_starts) ||
+        (num_pages > 0 && !kv_pool) || (pages_per_seq > 0 && !block_table))
+        return RQ_ERR_NULL;
+    if (workspace_bytes < rq::paged_attn_workspace_bytes(n_q_heads, n_kv_heads)) return RQ_ERR_SHAPE;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(kv_pool) || !aligned16(workspace) ||
+        !aligned4(q_starts) || !aligned4(kv_lens) || !aligned4(block_table) || !aligned4(d_k_gs) ||
+        !aligned4(d_v_gs) || !aligned4(lse))
+        return RQ_ERR_MISALIGNED;
+    const Span ins[] = {
+        span(q, ((n_tokens - 1) * q_token_stride + (int64_t)n_q_heads * head_dim) * 2),
+        span(kv_pool, pool_bytes(num_pages, page_size, n_kv_heads)),
+        span(block_table, pages_per_seq > 0 ? ((n_seqs - 1) * table_stride + pages_per_seq) * 4 : 0),
+        span(q_starts, (n_seqs + 1) * 4),
+        span(kv_lens, n_seqs * 4),
+        span(d_k_gs, 4),
+        span(d_v_gs, 4)};
+    const Span outs[] = {span(out, n_tokens * n_q_heads * (int64_t)head_dim * 2),
+                         span(lse, n_tokens * n_q_heads * (int64_t)4),
+                         span(workspace, (int64_t)rq::paged_attn_workspace_bytes(n_q_heads, n_kv_heads))};
+    if (bad_alias(outs, 3, ins, 7)) return RQ_ERR_ALIAS;
+
+    rq::PagedAttnParams p = {};
+    p.q = q;
+    p.q_stride = q_token_stride;
+    p.n_tokens = n_tokens;
+    p.hq = n_q_heads;
+    p.hk = n_kv_heads;
+    p.per = n_q_heads / n_kv_heads;
+    p.pool = kv_pool;
+    p.num_pages = num_pages;
+    p.groups = page_size / 16;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.max_keys = (int)(pages_per_seq * page_size);
+    p.q_starts = q_starts;
+    p.kv_lens = kv_lens;
+    p.n_seqs = (int)n_seqs;
+    p.max_q = (int)(max_q_len < n_tokens ? max_q_len : n_tokens);
+    p.scale = sm_scale * 1.44269504088896340736f;
+    p.window = window;
+    p.k_gs = d_k_gs;
+    p.v_gs = d_v_gs;
+    p.out = out;
+    p.lse = lse;
+    p.workspace = static_cast<uint8_t *>(workspace);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_status(dt == RQ_BF16 ? rq::launch_paged_attn<rq::BF16>(p, s)
+                                     : rq::launch_paged_attn<rq::FP16>(p, s));
+}
+
 }  // namespace
 
 extern "C" {
@@ -598,6 +685,131 @@ rq_status rq_qk_rmsnorm_rope_fp8_dynamic(const void *q, const void *k, int64_t q
     return qk_call(q, k, q_token_stride, k_token_stride, n_tokens, n_q_heads, n_k_heads, head_dim,
                    q_weight, k_weight, eps, positions, cos_sin_cache, max_pos, d_q_scale_out,
                    d_k_scale_out, q_out, k_out, QKCall{}, dt, stream);
+}
+
+rq_status rq_qkv_rope_nvfp4_kv_append(
+    const void *q, const void *k, const void *v, int64_t q_token_stride, int64_t k_token_stride,
+    int64_t v_token_stride, int64_t n_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+    const void *q_weight, const void *k_weight, float eps, const int32_t *positions,
+    const float *cos_sin_cache, int64_t max_pos, const float *d_k_global_scale,
+    const float *d_v_global_scale, void *q_out, uint8_t *kv_pool, int64_t num_pages, int page_size,
+    const int64_t *slots, rq_dtype dt, rq_stream_t stream)
+{
+    if (dt != RQ_BF16 && dt != RQ_FP16) return RQ_ERR_DTYPE;
+    if (n_tokens < 0 || n_tokens > (int64_t)1 << 36 || n_q_heads < 0 || n_kv_heads < 0 ||
+        n_q_heads > RQ_QK_MAX_HEADS || n_kv_heads > RQ_QK_MAX_HEADS || max_pos < 1 ||
+        max_pos > (int64_t)1 << 40)
+        return RQ_ERR_SHAPE;
+    if (head_dim != RQ_QK_HEAD_DIM) return RQ_ERR_UNSUPPORTED;
+    const bool has_q = n_q_heads > 0, has_k = n_kv_heads > 0;
+    if (has_k && !valid_pool(num_pages, page_size, n_kv_heads)) return RQ_ERR_SHAPE;
+    if (n_tokens == 0 || (!has_q && !has_k)) return RQ_OK;
+    const int64_t strides[] = {q_token_stride, k_token_stride, v_token_stride};
+    for (int i = 0; i < 3; ++i) {
+        const int heads = i == 0 ? n_q_heads : n_kv_heads;
+        if (heads == 0) continue;
+        if (strides[i] % 8 != 0) return RQ_ERR_MISALIGNED;
+        if (strides[i] < (int64_t)heads * head_dim || strides[i] > (int64_t)1 << 40) return RQ_ERR_SHAPE;
+    }
+    if (!positions || !cos_sin_cache || (has_q && (!q || !q_out)) ||
+        (has_k && (!k || !v || !d_k_global_scale || !d_v_global_scale || !kv_pool || !slots)))
+        return RQ_ERR_NULL;
+    if (!aligned16(cos_sin_cache) || !aligned4(positions) ||
+        (has_q && (!aligned16(q) || !aligned16(q_out) || !aligned16(q_weight))) ||
+        (has_k && (!aligned16(k) || !aligned16(v) || !aligned16(k_weight) || !aligned16(kv_pool) ||
+                   !aligned4(d_k_global_scale) || !aligned4(d_v_global_scale) ||
+                   (reinterpret_cast<uintptr_t>(slots) & 7u))))
+        return RQ_ERR_MISALIGNED;
+    auto extent = [&](int64_t stride, int heads) {
+        return ((n_tokens - 1) * stride + (int64_t)heads * head_dim) * 2;
+    };
+    const Span ins[] = {span(has_q ? q : nullptr, extent(q_token_stride, n_q_heads)),
+                        span(has_k ? k : nullptr, extent(k_token_stride, n_kv_heads)),
+                        span(has_k ? v : nullptr, extent(v_token_stride, n_kv_heads)),
+                        span(has_q ? q_weight : nullptr, head_dim * 2),
+                        span(has_k ? k_weight : nullptr, head_dim * 2),
+                        span(positions, n_tokens * 4),
+                        span(cos_sin_cache, max_pos * head_dim * 4),
+                        span(has_k ? d_k_global_scale : nullptr, 4),
+                        span(has_k ? d_v_global_scale : nullptr, 4),
+                        span(has_k ? slots : nullptr, n_tokens * 8)};
+    const Span outs[] = {span(has_q ? q_out : nullptr, n_tokens * n_q_heads * (int64_t)head_dim * 2),
+                         span(has_k ? kv_pool : nullptr, pool_bytes(num_pages, page_size, n_kv_heads))};
+    if (bad_alias(outs, 2, ins, 10)) return RQ_ERR_ALIAS;
+
+    rq::KVAppendParams p = {};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_stride = q_token_stride;
+    p.k_stride = k_token_stride;
+    p.v_stride = v_token_stride;
+    p.n_tokens = n_tokens;
+    p.hq = n_q_heads;
+    p.hk = n_kv_heads;
+    p.qw = q_weight;
+    p.kw = k_weight;
+    p.eps = eps;
+    p.pos = positions;
+    p.cos_sin = cos_sin_cache;
+    p.max_pos = max_pos;
+    p.k_gs = d_k_global_scale;
+    p.v_gs = d_v_global_scale;
+    p.q_out = q_out;
+    p.pool = kv_pool;
+    p.slots = slots;
+    p.num_slots = has_k ? num_pages * page_size : 0;
+    p.groups = has_k ? page_size / 16 : 1;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return cuda_status(dt == RQ_BF16 ? rq::launch_kv_append<rq::BF16>(p, s)
+                                     : rq::launch_kv_append<rq::FP16>(p, s));
+}
+
+rq_status rq_paged_decode_attn_nvfp4(const void *q, int64_t q_token_stride, int64_t n_seqs,
+                                     int n_q_heads, int n_kv_heads, int head_dim,
+                                     const uint8_t *kv_pool, int64_t num_pages, int page_size,
+                                     const int32_t *block_table, int64_t table_stride,
+                                     int64_t pages_per_seq, const int32_t *kv_lens, float sm_scale,
+                                     int window, const float *d_k_global_scale,
+                                     const float *d_v_global_scale, void *out, float *lse,
+                                     void *workspace, size_t workspace_bytes, rq_dtype dt,
+                                     rq_stream_t stream)
+{
+    return attn_call(q, q_token_stride, n_seqs, nullptr, n_seqs, 1, n_q_heads, n_kv_heads, head_dim,
+                     kv_pool, num_pages, page_size, block_table, table_stride, pages_per_seq, kv_lens,
+                     sm_scale, window, d_k_global_scale, d_v_global_scale, out, lse, workspace,
+                     workspace_bytes, dt, stream, false);
+}
+
+rq_status rq_paged_extend_attn_nvfp4(const void *q, int64_t q_token_stride, int64_t n_tokens,
+                                     const int32_t *q_starts, int64_t n_seqs, int64_t max_q_len,
+                                     int n_q_heads, int n_kv_heads, int head_dim,
+                                     const uint8_t *kv_pool, int64_t num_pages, int page_size,
+                                     const int32_t *block_table, int64_t table_stride,
+                                     int64_t pages_per_seq, const int32_t *kv_lens, float sm_scale,
+                                     int window, const float *d_k_global_scale,
+                                     const float *d_v_global_scale, void *out, float *lse,
+                                     void *workspace, size_t workspace_bytes, rq_dtype dt,
+                                     rq_stream_t stream)
+{
+    return attn_call(q, q_token_stride, n_tokens, q_starts, n_seqs, max_q_len, n_q_heads, n_kv_heads,
+                     head_dim, kv_pool, num_pages, page_size, block_table, table_stride,
+                     pages_per_seq, kv_lens, sm_scale, window, d_k_global_scale, d_v_global_scale,
+                     out, lse, workspace, workspace_bytes, dt, stream, true);
+}
+
+size_t rq_paged_attn_nvfp4_workspace_bytes(int n_q_heads, int n_kv_heads)
+{
+    return n_q_heads > 0 && n_kv_heads > 0 && n_q_heads % n_kv_heads == 0
+               ? rq::paged_attn_workspace_bytes(n_q_heads, n_kv_heads)
+               : 0;
+}
+
+size_t rq_nvfp4_kv_page_bytes(int page_size)
+{
+    return page_size > 0 && page_size % 16 == 0 && page_size <= RQ_KV_MAX_PAGE
+               ? (size_t)page_size / 16 * rq::kKVGroupBytes
+               : 0;
 }
 
 size_t rq_nvfp4_packed_bytes(int64_t rows, int64_t hidden)

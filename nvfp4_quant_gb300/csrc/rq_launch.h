@@ -125,6 +125,62 @@ cudaError_t launch_add_rmsnorm(const NormQuantParams &p, cudaStream_t stream);
 template <typename DT, int QMODE>
 cudaError_t launch_qk_rmsnorm_rope(const QKParams &p, cudaStream_t stream);
 
+// ---- NVFP4 KV cache: page p, head h, token t of the page lie in group
+// (p * heads + h) * (page_size / 16) + t / 16 of 2304 bytes; inside a group,
+// row t % 16 of the parts below (64 bytes a row of codes, 8 of scales).
+constexpr int kKVGroupBytes = 2304;
+constexpr int kKVCodesK = 0, kKVCodesV = 1024, kKVScalesK = 2048, kKVScalesV = 2176;
+
+struct KVAppendParams {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;  // elements between tokens
+    int64_t n_tokens;
+    int hq, hk;
+    const void *qw, *kw;     // null: no norm
+    float eps;
+    const int32_t *pos;
+    const float *cos_sin;
+    int64_t max_pos;
+    const float *k_gs, *v_gs;
+    void *q_out;
+    uint8_t *pool;
+    const int64_t *slots;
+    int64_t num_slots;       // num_pages * page_size
+    int groups;              // page_size / 16
+};
+
+template <typename DT>
+cudaError_t launch_kv_append(const KVAppendParams &p, cudaStream_t stream);
+
+struct PagedAttnParams {
+    const void *q;
+    int64_t q_stride;          // elements between tokens
+    int64_t n_tokens;          // rows of q and out
+    int hq, hk, per;           // per = hq / hk query heads share a KV head
+    const uint8_t *pool;
+    int64_t num_pages;
+    int groups;                // page_size / 16
+    const int32_t *table;      // page ids, [n_seqs, table_stride]
+    int64_t table_stride;
+    int max_keys;              // pages_per_seq * page_size: kv_lens are clamped to it
+    const int32_t *q_starts;   // null: one query per sequence
+    const int32_t *kv_lens;
+    int n_seqs;
+    int max_q;                 // caller's bound on query lengths (a hint)
+    float scale;               // sm_scale * log2(e)
+    int window;                // 0: none
+    const float *k_gs, *v_gs;
+    void *out;                 // [n_tokens, hq, 128]
+    float *lse;                // [n_tokens, hq] or null
+    uint8_t *workspace;
+};
+
+// Bytes of PagedAttnParams::workspace.
+size_t paged_attn_workspace_bytes(int hq, int hk);
+
+template <typename DT>
+cudaError_t launch_paged_attn(const PagedAttnParams &p, cudaStream_t stream);
+
 // out = amax / 448 (nvfp4 == 0) or 2688 / amax (nvfp4 == 1); with
 // zero_to_one, a zero amax gives 1.  out may equal amax.
 cudaError_t launch_scale_from_amax(const float *amax, float *out, int nvfp4, int zero_to_one,

@@ -1,0 +1,678 @@
+// rq_paged_attn.cu -- attention over the paged NVFP4 cache for few queries a
+// sequence (single-token decode, drafted tokens): the keys of a sequence are
+// split over CTAs, each CTA's share over its warps, and the parts joined.
+//
+// Mathematics.  With x_j = scale log2(e) q . k_j, a part of the keys gives
+//   m >= max x_j - 8,  l = sum 2^(x_j - m),  O = sum 2^(x_j - m) v_j
+// and parts join by (m, l, O) -> sum of 2^(m_i - m) (l_i, O_i).  m is moved
+// only when some x exceeds it by more than 8 (the fp16 probabilities then stay
+// below 2^8), so most tiles need no reduction over lanes.
+//
+// What bounds it: 144 bytes a key and KV head have to come from HBM; at 6.8
+// TB/s an SM gets one every 6.1 clocks.  The products run on mma.sync with
+// keys (then channels) as its 16 rows and queries as its 8 columns: the 2
+// clocks a key that this takes at 8 columns lie under the memory time, and a
+// key's codes go from shared memory to registers as the operand itself.
+// (tcgen05 would want the decoded tile written to shared memory first, 512
+// bytes a key: 4 clocks.)  Decoding (e2m1x2 -> f16x2, times the scale, exact)
+// and the rest issue about 14 warp instructions a key, 3.5 clocks.
+//
+// Tokens of a group of 16 are laid over the fragments so that no value moves
+// between lanes: lane (g, c) = (lane / 4, lane % 4) holds
+//   K (16 tokens x 128, A operand): tokens row g and g + 8, channels 32 c ..
+//     32 c + 31 (16 bytes of codes, 2 scales) over the 8 products;
+//   V^T (128 x 16 tokens, A operand): channels 16 g .. 16 g + 15 (8 bytes of
+//     codes, 1 scale) of tokens c, 4 + c, 8 + c, 12 + c; the nibbles of two
+//     tokens are interleaved before the conversion, which then yields token
+//     pairs;
+//   S^T rows are the tokens, turned into the B operand of the second product
+//     by movmatrix.  Row r of the first product is token tok(r) below.
+#include "rq_device.cuh"
+#include "rq_launch.h"
+
+#include <atomic>
+#include <type_traits>
+
+namespace rq {
+
+namespace {
+
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kChunkGroups = 2, kChunk = kChunkGroups * 16;  // keys of one step of a warp
+constexpr int kStages = 3;
+constexpr int kChunkBytes = kChunkGroups * kKVGroupBytes;
+constexpr int kSmem = kWarps * kStages * kChunkBytes;
+constexpr int kMaxCtas = 512;      // grid limit (workspace slots)
+constexpr float kNone = -3.0e38f;  // m of a part without keys
+constexpr float kRaise = 8.0f;
+
+// A part: O [8 NT][128], m [8 NT], l [8 NT].
+template <int NT>
+constexpr int kPartFloats = 8 * NT * (128 + 2);
+
+// What the CTA left for the join, two slots each: slot 0 a part that continues
+// an item begun by an earlier CTA (last: it ends it), slot 1 the first part of
+// an item that later CTAs continue.
+struct PartInfo {
+    int valid, last, seq, head, block;
+};
+
+constexpr size_t kInfoBytes = ((size_t)kMaxCtas * 2 * sizeof(PartInfo) + 15) / 16 * 16;
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+template <int B>
+__device__ __forceinline__ uint32_t e2m1_pair(uint32_t w)  // byte B of w -> f16x2
+{
+    uint32_t d;
+    if (B == 0) asm("{ .reg .b8 a, b, c, e; mov.b32 {a, b, c, e}, %1; cvt.rn.f16x2.e2m1x2 %0, a; }" : "=r"(d) : "r"(w));
+    if (B == 1) asm("{ .reg .b8 a, b, c, e; mov.b32 {a, b, c, e}, %1; cvt.rn.f16x2.e2m1x2 %0, b; }" : "=r"(d) : "r"(w));
+    if (B == 2) asm("{ .reg .b8 a, b, c, e; mov.b32 {a, b, c, e}, %1; cvt.rn.f16x2.e2m1x2 %0, c; }" : "=r"(d) : "r"(w));
+    if (B == 3) asm("{ .reg .b8 a, b, c, e; mov.b32 {a, b, c, e}, %1; cvt.rn.f16x2.e2m1x2 %0, e; }" : "=r"(d) : "r"(w));
+    return d;
+}
+
+// two E4M3 bytes (low half of w) -> f16x2
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w)
+{
+    uint32_t d;
+    asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(d) : "r"(w));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t lds_u16(const uint8_t *s)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(smem_addr(s)) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(const uint8_t *s)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(smem_addr(s)) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(const uint8_t *s)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(smem_addr(s)) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                 "{%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
+{
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
+}
+
+// Token of row r of the first product (r < 8; r + 8 is 8 tokens further), and
+// its inverse: where a token's 64 bytes of K codes are put, so that a warp's
+// 16-byte reads by row are consecutive.
+__device__ __forceinline__ int tok_of_row(int r) { return (r & 1) * 4 + (r >> 1); }
+__device__ __forceinline__ int row_of_tok(int t) { return (t >> 3) * 8 + (t & 3) * 2 + ((t >> 2) & 1); }
+
+struct Seq {
+    int q0, nq, first_pos, lo, hi, tiles, blocks;
+};
+
+// Sequence b's queries and the keys they can see, in chunks from lo.
+template <int NT>
+__device__ __forceinline__ Seq load_seq(const PagedAttnParams &p, int b)
+{
+    Seq s;
+    if (p.q_starts != nullptr) {
+        const int a = ld_s32(p.q_starts + b), z = ld_s32(p.q_starts + b + 1);
+        s.q0 = min(max(a, 0), (int)p.n_tokens);
+        s.nq = min(max(z, s.q0), (int)p.n_tokens) - s.q0;
+    } else {
+        s.q0 = b;
+        s.nq = 1;
+    }
+    s.hi = min(max(ld_s32(p.kv_lens + b), 0), p.max_keys);
+    s.first_pos = s.hi - s.nq;
+    s.lo = p.window > 0 ? max(0, s.first_pos - p.window + 1) & ~15 : 0;
+    s.tiles = s.hi > s.lo ? (s.hi - s.lo + kChunk - 1) / kChunk : 1;
+    s.blocks = (s.nq * p.per + 8 * NT - 1) / (8 * NT);
+    return s;
+}
+
+template <int NT>
+__device__ __forceinline__ int64_t seq_units(const PagedAttnParams &p, const Seq &s)
+{
+    return (int64_t)p.hk * s.blocks * s.tiles;
+}
+
+// Stores 8 NT columns' results: out (and lse) of column col from its sums.
+template <typename DT, int VALS>
+__device__ __forceinline__ void store_out(const PagedAttnParams &p, const Seq &s, int head, int col,
+                                          int d0, float (&v)[VALS], float m, float l)
+{
+    const int i = col / p.per, h = head * p.per + col % p.per;
+    const int64_t row = ((int64_t)(s.q0 + i) * p.hq + h);
+    const float inv = l > 0.0f ? 1.0f / (l * ld_f32(p.v_gs)) : (l == 0.0f ? 0.0f : l);
+    uint8_t *dst = static_cast<uint8_t *>(p.out) + (row * 128 + d0) * 2;
+#pragma unroll
+    for (int k = 0; k < VALS; k += 4)
+        *reinterpret_cast<uint2 *>(dst + 2 * k) =
+            make_uint2(DT::pack(v[k] * inv, v[k + 1] * inv), DT::pack(v[k + 2] * inv, v[k + 3] * inv));
+    if (p.lse != nullptr && d0 == 0)
+        p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+}
+
+template <typename DT, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
+paged_attn_split_kernel(const PagedAttnParams p)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ int64_t scan[kWarps];
+    __shared__ int start_seq;
+    __shared__ int64_t start_rem;
+    __shared__ float2 stats[kWarps][8 * NT];
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, c = lane & 3;
+    PartInfo *info = reinterpret_cast<PartInfo *>(p.workspace) + 2 * blockIdx.x;
+    float *parts = reinterpret_cast<float *>(p.workspace + kInfoBytes) +
+                   (int64_t)blockIdx.x * 2 * kPartFloats<NT>;
+
+    // ---- this CTA's share: units (head, block, chunk of keys) of all
+    // sequences in order, cut into equal runs.  Thread t adds up the units of
+    // its run of sequences; the thread whose run holds the first unit finds it.
+    const int per_thread = (p.n_seqs + kThreads - 1) / kThreads;
+    const int b0 = min(p.n_seqs, (int)threadIdx.x * per_thread), b1 = min(p.n_seqs, b0 + per_thread);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += seq_units<NT>(p, load_seq<NT>(p, b));
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) scan[warp] = upto;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w == warp) upto += total;
+        total += scan[w];
+    }
+    // at least a chunk per warp, where there is enough
+    const int64_t n = max((int64_t)1, min((int64_t)gridDim.x, total / kWarps));
+    const int64_t i0 = blockIdx.x;
+    int64_t u = i0 < n ? total * i0 / n : total;
+    const int64_t u_end = i0 < n ? total * (i0 + 1) / n : total;
+    if (upto - mine <= u && u < upto) {
+        int64_t rem = u - (upto - mine);
+        int b = b0;
+        for (;; ++b) {
+            const int64_t w = seq_units<NT>(p, load_seq<NT>(p, b));
+            if (rem < w) break;
+            rem -= w;
+        }
+        start_seq = b;
+        start_rem = rem;
+    }
+    if (threadIdx.x < 2) info[threadIdx.x].valid = 0;
+    __syncthreads();
+    if (u >= u_end) return;
+    int b = start_seq;
+    int64_t rem = start_rem;
+
+    uint8_t *ring = smem + warp * (kStages * kChunkBytes);
+    // where the lane's 16-byte pieces of a group go (the fifth: lanes 0-15)
+    const int kdst = row_of_tok(lane >> 2) * 64 + (lane & 3) * 16;  // + 512: tokens 8-15
+    const int vdst = kKVCodesV + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 1) * 2) * 16);
+    // where it reads them
+    const int kread = g * 64 + c * 16;
+    const int vread = kKVCodesV + c * 64 + (((g >> 1) ^ ((c >> 1) & 1) * 2) * 16) + (g & 1) * 8;
+    const int ksread = kKVScalesK + tok_of_row(g) * 8 + 2 * c;
+    const int vsread = kKVScalesV + c * 8 + g;
+    const float inv_kgs = 1.0f / ld_f32(p.k_gs);
+
+    Seq s = load_seq<NT>(p, b);
+    while (u < u_end) {
+        const int64_t all = seq_units<NT>(p, s);
+        if (rem >= all) {
+            rem -= all;
+            s = load_seq<NT>(p, ++b);
+            continue;
+        }
+        const int item = (int)(rem / s.tiles), tile0 = (int)(rem - (int64_t)item * s.tiles);
+        const int head = item / s.blocks, block = item - head * s.blocks;
+        const int ntile = (int)min((int64_t)(s.tiles - tile0), u_end - u);
+        const int col0 = block * 8 * NT, cols = min(8 * NT, s.nq * p.per - col0);
+        // keys that the block's columns see: all of [need_lo, need_hi) by every
+        // one, nothing from blk_hi on by any
+        const int i_first = col0 / p.per, i_last = (col0 + cols - 1) / p.per;
+        const int blk_hi = s.first_pos + i_last + 1;
+        const int need_hi = s.first_pos + i_first + 1;
+        const int need_lo = p.window > 0 ? blk_hi - p.window : 0;
+        const int t0 = s.lo + tile0 * kChunk;
+        const int t1 = min(blk_hi, t0 + ntile * kChunk);  // may lie before t0: nothing to do
+        const int chunks = t1 > t0 + warp * kChunk
+                               ? (t1 - t0 - warp * kChunk + kWarps * kChunk - 1) / (kWarps * kChunk)
+                               : 0;  // of this warp
+
+        // ---- queries: columns nt * 8 + g, channels 32 c .. + 31, as the B
+        // operand; each row by a power of two so that fp16 holds it
+        uint32_t qf[NT][16];
+        float cs[NT][2], m[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int col = nt * 8 + g;
+            uint4 v[4] = {};
+            if (col < cols) {
+                const int i = (col0 + col) / p.per, h = head * p.per + (col0 + col) % p.per;
+                const uint8_t *src = static_cast<const uint8_t *>(p.q) +
+                                     ((s.q0 + i) * p.q_stride + (int64_t)h * 128 + 32 * c) * 2;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = ld_keep16(src + 16 * k);
+            }
+            float f = 1.0f, back = 1.0f;
+            if (std::is_same<DT, BF16>::value) {
+                float a = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float e[8];
+                    unpack8<DT>(v[k], e);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(e[j]));
+                }
+                a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
+                a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
+                // 2^-e and 2^e of the largest element's exponent, kept normal
+                const int e = min(max((int)(__float_as_uint(a) >> 23) - 127, -126), 126);
+                f = __uint_as_float((uint32_t)(127 - e) << 23);
+                back = __uint_as_float((uint32_t)(127 + e) << 23);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float e[8];
+                unpack8<DT>(v[k], e);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) qf[nt][4 * k + j] = FP16::pack(e[2 * j] * f, e[2 * j + 1] * f);
+            }
+            const float scale = p.scale * inv_kgs * back;
+            cs[nt][0] = __shfl_sync(0xFFFFFFFFu, scale, 8 * c);
+            cs[nt][1] = __shfl_sync(0xFFFFFFFFu, scale, 8 * c + 4);
+            m[nt][0] = m[nt][1] = kNone;
+            l[nt][0] = l[nt][1] = 0.0f;
+        }
+        float o[NT][8][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.0f;
+
+        // ---- groups of the warp's chunks, 16 chunks at a time: lane 2 i + j
+        // holds where group j of chunk i lies in the cache (-1: nowhere)
+        auto find = [&](int batch) {
+            const int token = t0 + (warp + kWarps * (batch * 16 + (lane >> 1))) * kChunk + (lane & 1) * 16;
+            int at = -1;
+            if (token < t1) {
+                const int slot = token >> 4, page = slot / p.groups;
+                const int id = ld_s32(p.table + (int64_t)b * p.table_stride + page);
+                if (id >= 0 && id < p.num_pages)
+                    at = (int)(((int64_t)id * p.hk + head) * p.groups + (slot - page * p.groups));
+            }
+            return at;
+        };
+        int near = find(0), far = find(1);
+        auto fetch = [&](int i, int cur_batch) {  // starts the copies of chunk i
+            const int from = (i >> 4) == cur_batch ? near : far;
+            uint8_t *to = ring + (i % kStages) * kChunkBytes;
+#pragma unroll
+            for (int gr = 0; gr < kChunkGroups; ++gr) {
+                const int at = __shfl_sync(0xFFFFFFFFu, from, (i & 15) * 2 + gr);
+                if (at >= 0 && i < chunks) {
+                    const uint8_t *src = p.pool + (int64_t)at * kKVGroupBytes + lane * 16;
+                    uint8_t *d = to + gr * kKVGroupBytes;
+                    cp_async16(d + kdst, src);
+                    cp_async16(d + kdst + 512, src + 512);
+                    cp_async16(d + vdst, src + 1024);
+                    cp_async16(d + vdst + 512, src + 1536);
+                    if (lane < 16) cp_async16(d + 2048 + lane * 16, src + 2048);
+                }
+            }
+            cp_async_commit();
+        };
+        for (int i = 0; i < kStages - 1; ++i) fetch(i, 0);
+
+        for (int it = 0; it < chunks; ++it) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();  // everyone's copies have landed; everyone is done with the stage before
+            if (it > 0 && (it & 15) == 0) {
+                near = far;
+                far = find((it >> 4) + 1);
+            }
+            fetch(it + kStages - 1, it >> 4);
+            const uint8_t *stage = ring + (it % kStages) * kChunkBytes;
+            const int tok0 = t0 + (warp + kWarps * it) * kChunk;
+            bool here[kChunkGroups], full = tok0 >= need_lo && tok0 + kChunk <= need_hi;
+#pragma unroll
+            for (int gr = 0; gr < kChunkGroups; ++gr) {
+                here[gr] = __shfl_sync(0xFFFFFFFFu, near, (it & 15) * 2 + gr) >= 0;
+                full &= here[gr];
+            }
+
+            // ---- S^T = K Q^T
+            float x[kChunkGroups][NT][4];
+#pragma unroll
+            for (int gr = 0; gr < kChunkGroups; ++gr) {
+                const uint8_t *base = stage + gr * kKVGroupBytes;
+                const uint4 ka = lds16(base + kread), kb = lds16(base + kread + 512);
+                const uint32_t sa = e4m3_pair(lds_u16(base + ksread));
+                const uint32_t sb = e4m3_pair(lds_u16(base + ksread + 64));
+                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[gr][nt][e] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t fa = __byte_perm(sa, sa, k < 2 ? 0x1010 : 0x3232);
+                    const uint32_t fb = __byte_perm(sb, sb, k < 2 ? 0x1010 : 0x3232);
+                    const uint32_t a0 = FP16::mul2(e2m1_pair<0>(wa[k]), fa);
+                    const uint32_t a1 = FP16::mul2(e2m1_pair<0>(wb[k]), fb);
+                    const uint32_t a2 = FP16::mul2(e2m1_pair<1>(wa[k]), fa);
+                    const uint32_t a3 = FP16::mul2(e2m1_pair<1>(wb[k]), fb);
+                    const uint32_t a4 = FP16::mul2(e2m1_pair<2>(wa[k]), fa);
+                    const uint32_t a5 = FP16::mul2(e2m1_pair<2>(wb[k]), fb);
+                    const uint32_t a6 = FP16::mul2(e2m1_pair<3>(wa[k]), fa);
+                    const uint32_t a7 = FP16::mul2(e2m1_pair<3>(wb[k]), fb);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma(x[gr][nt], a0, a1, a2, a3, qf[nt][4 * k], qf[nt][4 * k + 1]);
+                        mma(x[gr][nt], a4, a5, a6, a7, qf[nt][4 * k + 2], qf[nt][4 * k + 3]);
+                    }
+                }
+            }
+
+            // ---- probabilities 2^(x - m)
+            uint32_t hidden = 0;  // bit (gr, nt, e): the key is not seen by the column
+            if (!full) {
+#pragma unroll
+                for (int gr = 0; gr < kChunkGroups; ++gr)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int t = tok0 + gr * 16 + tok_of_row(g) + (e >> 1) * 8;
+                            const int col = nt * 8 + 2 * c + (e & 1);
+                            const int pos = s.first_pos + (col0 + col) / p.per;
+                            const bool seen = here[gr] && col < cols && t <= pos &&
+                                              (p.window == 0 || t > pos - p.window);
+                            hidden |= (uint32_t)!seen << ((gr * NT + nt) * 4 + e);
+                        }
+            }
+            float y[kChunkGroups][NT][4];
+            bool high = false;
+#pragma unroll
+            for (int gr = 0; gr < kChunkGroups; ++gr)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v = fmaf(x[gr][nt][e], cs[nt][e & 1], -m[nt][e & 1]);
+                        if (hidden & (1u << ((gr * NT + nt) * 4 + e))) v = -INFINITY;
+                        y[gr][nt][e] = v;
+                        high |= v > kRaise;
+                    }
+            if (__any_sync(0xFFFFFFFFu, high)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float top = kNone;
+#pragma unroll
+                        for (int gr = 0; gr < kChunkGroups; ++gr)
+#pragma unroll
+                            for (int e = k; e < 4; e += 2)
+                                if (!(hidden & (1u << ((gr * NT + nt) * 4 + e))))
+                                    top = fmaxf(top, x[gr][nt][e] * cs[nt][k]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                        const float now = fmaxf(m[nt][k], top);
+                        const float f = ex2(m[nt][k] - now);
+                        m[nt][k] = now;
+                        l[nt][k] *= f;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            o[nt][j][k] *= f;
+                            o[nt][j][k + 2] *= f;
+                        }
+#pragma unroll
+                        for (int gr = 0; gr < kChunkGroups; ++gr)
+#pragma unroll
+                            for (int e = k; e < 4; e += 2)
+                                y[gr][nt][e] = hidden & (1u << ((gr * NT + nt) * 4 + e))
+                                                   ? -INFINITY
+                                                   : fmaf(x[gr][nt][e], cs[nt][k], -now);
+                    }
+            }
+            uint32_t pf[kChunkGroups][NT][2];
+#pragma unroll
+            for (int gr = 0; gr < kChunkGroups; ++gr)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        y[gr][nt][e] = ex2(y[gr][nt][e]);
+                        l[nt][e & 1] += y[gr][nt][e];
+                    }
+                    pf[gr][nt][0] = transpose8x8(FP16::pack(y[gr][nt][0], y[gr][nt][1]));
+                    pf[gr][nt][1] = transpose8x8(FP16::pack(y[gr][nt][2], y[gr][nt][3]));
+                }
+
+            // ---- O^T += V^T P^T
+#pragma unroll
+            for (int gr = 0; gr < kChunkGroups; ++gr) {
+                const uint8_t *base = stage + gr * kKVGroupBytes;
+                const uint2 v0 = lds8(base + vread), v1 = lds8(base + vread + 256);
+                const uint2 v2 = lds8(base + vread + 512), v3 = lds8(base + vread + 768);
+                uint32_t f01 = lds_u8(base + vsread) | (lds_u8(base + vsread + 32) << 8);
+                uint32_t f23 = lds_u8(base + vsread + 64) | (lds_u8(base + vsread + 96) << 8);
+                if (!full) {  // bytes of keys that nobody sees may be anything
+                    const int t = tok0 + gr * 16 + c;
+                    const int end = here[gr] ? blk_hi : 0;
+                    if (t >= end) f01 &= 0xFF00u;
+                    if (t + 4 >= end) f01 &= 0x00FFu;
+                    if (t + 8 >= end) f23 &= 0xFF00u;
+                    if (t + 12 >= end) f23 &= 0x00FFu;
+                }
+                const uint32_t sa = e4m3_pair(f01), sb = e4m3_pair(f23);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t w0 = k ? v0.y : v0.x, w1 = k ? v1.y : v1.x;
+                    const uint32_t w2 = k ? v2.y : v2.x, w3 = k ? v3.y : v3.x;
+                    const uint32_t lo = 0x0F0F0F0Fu;
+                    const uint32_t ea = (w0 & lo) | ((w1 << 4) & ~lo), oa = ((w0 >> 4) & lo) | (w1 & ~lo);
+                    const uint32_t eb = (w2 & lo) | ((w3 << 4) & ~lo), ob = ((w2 >> 4) & lo) | (w3 & ~lo);
+#define RQ_PV(B)                                                                                     \
+    {                                                                                                \
+        const uint32_t a0 = FP16::mul2(e2m1_pair<B>(ea), sa), a1 = FP16::mul2(e2m1_pair<B>(oa), sa); \
+        const uint32_t a2 = FP16::mul2(e2m1_pair<B>(eb), sb), a3 = FP16::mul2(e2m1_pair<B>(ob), sb); \
+        _Pragma("unroll") for (int nt = 0; nt < NT; ++nt)                                            \
+            mma(o[nt][4 * k + B], a0, a1, a2, a3, pf[gr][nt][0], pf[gr][nt][1]);                     \
+    }
+                    RQ_PV(0)
+                    RQ_PV(1)
+                    RQ_PV(2)
+                    RQ_PV(3)
+#undef RQ_PV
+                }
+            }
+        }
+
+        // ---- join the warps: O of column k in the warp's ring, 512 bytes each
+        cp_async_wait<0>();
+        __syncwarp();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                float sum = l[nt][k];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+                const int col = nt * 8 + 2 * c + k;
+                if (g == 0) stats[warp][col] = make_float2(m[nt][k], sum);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<float2 *>(ring + col * 512 + (16 * g + 2 * j) * 4) =
+                        make_float2(o[nt][j][k], o[nt][j][k + 2]);
+            }
+        __syncthreads();
+        constexpr int kPerCol = kThreads / (8 * NT), kVals = 128 / kPerCol;
+        const int col = threadIdx.x / kPerCol, d0 = (threadIdx.x % kPerCol) * kVals;
+        if (col < cols) {
+            float top = kNone, sum = 0.0f, v[kVals] = {};
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[w][col].x);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = ex2(stats[w][col].x - top);
+                sum += f * stats[w][col].y;
+                const float *src = reinterpret_cast<const float *>(smem + w * (kStages * kChunkBytes) +
+                                                                   col * 512) + d0;
+#pragma unroll
+                for (int k = 0; k < kVals; ++k) v[k] = fmaf(f, src[k], v[k]);
+            }
+            if (ntile == s.tiles) {
+                store_out<DT, kVals>(p, s, head, col0 + col, d0, v, top, sum);
+            } else {
+                float *part = parts + (tile0 == 0 ? kPartFloats<NT> : 0);
+#pragma unroll
+                for (int k = 0; k < kVals; ++k) part[col * 128 + d0 + k] = v[k];
+                if (d0 == 0) {
+                    part[8 * NT * 128 + col] = top;
+                    part[8 * NT * 129 + col] = sum;
+                }
+            }
+        }
+        if (threadIdx.x == 0 && ntile != s.tiles)
+            info[tile0 == 0] = PartInfo{1, tile0 + ntile == s.tiles, b, head, block};
+        __syncthreads();
+        u += ntile;
+        rem += ntile;
+    }
+}
+
+// Joins the parts of items that CTAs of the kernel above share.  CTA i looks
+// at the item whose first part CTA i of that kernel left, if any, and at the
+// parts of the CTAs after it up to the one that ends the item.  A warp takes
+// columns of the item, a lane 4 channels.
+template <typename DT, int NT>
+__global__ void __launch_bounds__(256)
+paged_attn_join_kernel(const PagedAttnParams p, int ctas)
+{
+    __shared__ int last;
+    pdl_trigger();
+    pdl_wait();
+    const PartInfo *info = reinterpret_cast<const PartInfo *>(p.workspace);
+    const int i = blockIdx.x;
+    const PartInfo me = info[2 * i + 1];
+    if (!me.valid) return;
+    if (threadIdx.x == 0) last = ctas - 1;
+    __syncthreads();
+    for (int j = i + 1 + threadIdx.x; j < ctas; j += blockDim.x)
+        if (info[2 * j].valid && info[2 * j].last) atomicMin(&last, j);
+    __syncthreads();
+    const int end = last, n = end - i + 1;
+    const float *parts = reinterpret_cast<const float *>(p.workspace + kInfoBytes);
+    auto part = [&](int k) {  // the k-th part of the item
+        return parts + ((int64_t)(i + k) * 2 + (k == 0)) * kPartFloats<NT>;
+    };
+    const Seq s = load_seq<NT>(p, me.seq);
+    const int lane = threadIdx.x & 31, d0 = lane * 4;
+    for (int col = threadIdx.x >> 5; col < 8 * NT; col += 8) {
+        const int at = me.block * 8 * NT + col;
+        if (at >= s.nq * p.per) break;
+        float top = kNone;
+        for (int k = lane; k < n; k += 32) top = fmaxf(top, part(k)[8 * NT * 128 + col]);
+        top = group_max<32>(top);
+        float sum = 0.0f, v[4] = {};
+        constexpr int kU = 8;
+        for (int k0 = 0; k0 < n; k0 += kU) {
+            float4 a[kU];
+            float f[kU], ll[kU];
+#pragma unroll
+            for (int k = 0; k < kU; ++k) {
+                const float *src = part(min(k0 + k, n - 1));
+                a[k] = *reinterpret_cast<const float4 *>(src + col * 128 + d0);
+                f[k] = src[8 * NT * 128 + col];
+                ll[k] = src[8 * NT * 129 + col];
+            }
+#pragma unroll
+            for (int k = 0; k < kU; ++k) {
+                const float w = k0 + k < n ? ex2(f[k] - top) : 0.0f;
+                sum = fmaf(w, ll[k], sum);
+                v[0] = fmaf(w, a[k].x, v[0]);
+                v[1] = fmaf(w, a[k].y, v[1]);
+                v[2] = fmaf(w, a[k].z, v[2]);
+                v[3] = fmaf(w, a[k].w, v[3]);
+            }
+        }
+        store_out<DT, 4>(p, s, me.head, at, d0, v, top, sum);
+    }
+}
+
+template <typename DT, int NT>
+cudaError_t launch_split(const PagedAttnParams &p, int dev, cudaStream_t stream)
+{
+    static std::atomic<int> occ_cache[64];
+    auto kern = paged_attn_split_kernel<DT, NT>;
+    int per_sm = dev < 64 ? occ_cache[dev].load(std::memory_order_relaxed) : 0;
+    if (per_sm <= 0) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, kSmem);
+        if (e != cudaSuccess) return e;
+        if (per_sm < 1) return cudaErrorInvalidConfiguration;
+        if (dev < 64) occ_cache[dev].store(per_sm, std::memory_order_relaxed);
+    }
+    const int full = device_sms(dev) * per_sm, grid = full < kMaxCtas ? full : kMaxCtas;
+    cudaError_t e = launch_pdl(kern, grid, kThreads, kSmem, stream, p);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(paged_attn_join_kernel<DT, NT>, grid, 256, 0, stream, p, grid);
+}
+
+}  // namespace
+
+size_t paged_attn_workspace_bytes(int, int)
+{
+    return kInfoBytes + (size_t)kMaxCtas * 2 * kPartFloats<2> * sizeof(float);
+}
+
+template <typename DT>
+cudaError_t launch_paged_attn(const PagedAttnParams &p, cudaStream_t stream)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    // 8 columns hold the queries of a KV head, or 16 do (one pass over the
+    // keys instead of two)
+    return (int64_t)p.per * p.max_q <= 8 ? launch_split<DT, 1>(p, dev, stream)
+                                         : launch_split<DT, 2>(p, dev, stream);
+}
+
+template cudaError_t launch_paged_attn<BF16>(const PagedAttnParams &, cudaStream_t);
+template cudaError_t launch_paged_attn<FP16>(const PagedAttnParams &, cudaStream_t);
+
+}  // namespace rq
