@@ -407,7 +407,7 @@ rq_status rq_add_rmsnorm_nvfp4_dynamic_swizzled(
  *   (codes of signed zeros where sf = 0).
  * Unlike the calls above there is no intermediate rounding: q_out is fp32
  * arithmetic rounded once, and the codes are those of the real-valued formula
- * (decided in double precision wherever fp32 leaves a code open), so the bytes
+ * (decided in double-float arithmetic wherever fp32 leaves a code open), so the bytes
  * of the cache do not depend on any order of summation.
  * Source: "perf: add fused norm + RoPE + uniform fp8 store for TRT-LLM DSv4
  * sparse attention" (SGLang PR 32975), review thread, for the norm + RoPE +
