@@ -167,6 +167,7 @@ struct PagedAttnParams {
     const int32_t *kv_lens;
     int n_seqs;
     int max_q;                 // caller's bound on query lengths (a hint)
+    int few;                   // query columns of a sequence: up to it the split kernel
     float scale;               // sm_scale * log2(e)
     int window;                // 0: none
     const float *k_gs, *v_gs;

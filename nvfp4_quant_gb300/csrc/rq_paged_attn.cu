@@ -27,10 +27,10 @@
 //     pairs;
 //   S^T rows are the tokens, turned into the B operand of the second product
 //     by movmatrix.  Row r of the first product is token tok(r) below.
-#include "rq_device.cuh"
-#include "rq_launch.h"
+#include "rq_paged_attn.cuh"
 
 #include <atomic>
+#include <climits>
 #include <type_traits>
 
 namespace rq {
@@ -42,9 +42,10 @@ constexpr int kChunkGroups = 2, kChunk = kChunkGroups * 16;  // keys of one step
 constexpr int kStages = 3;
 constexpr int kChunkBytes = kChunkGroups * kKVGroupBytes;
 constexpr int kSmem = kWarps * kStages * kChunkBytes;
+// Queries x heads of a KV head up to which a sequence is taken here and not by
+// the tensor-memory kernel.
+constexpr int kFewColumns = 32;
 constexpr int kMaxCtas = 512;      // grid limit (workspace slots)
-constexpr float kNone = -3.0e38f;  // m of a part without keys
-constexpr float kRaise = 8.0f;
 
 // A part: O [8 NT][128], m [8 NT], l [8 NT].
 template <int NT>
@@ -58,32 +59,6 @@ struct PartInfo {
 };
 
 constexpr size_t kInfoBytes = ((size_t)kMaxCtas * 2 * sizeof(PartInfo) + 15) / 16 * 16;
-
-__device__ __forceinline__ float ex2(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-template <int B>
-__device__ __forceinline__ uint32_t e2m1_pair(uint32_t w)  // byte B of w -> f16x2
-{
-    uint32_t d;
-    if (B == 0) asm("{ .reg .b8 a, b, c, e; mov.b32 {a, b, c, e}, %1; cvt.rn.f16x2.e2m1x2 %0, a; }" : "=r"(d) : "r"(w));
-    if (B == 1) asm("{ .reg .b8 a, b, c, e; mov.b32 {a, b, c, e}, %1; cvt.rn.f16x2.e2m1x2 %0, b; }" : "=r"(d) : "r"(w));
-    if (B == 2) asm("{ .reg .b8 a, b, c, e; mov.b32 {a, b, c, e}, %1; cvt.rn.f16x2.e2m1x2 %0, c; }" : "=r"(d) : "r"(w));
-    if (B == 3) asm("{ .reg .b8 a, b, c, e; mov.b32 {a, b, c, e}, %1; cvt.rn.f16x2.e2m1x2 %0, e; }" : "=r"(d) : "r"(w));
-    return d;
-}
-
-// two E4M3 bytes (low half of w) -> f16x2
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t w)
-{
-    uint32_t d;
-    asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(d) : "r"(w));
-    return d;
-}
 
 __device__ __forceinline__ uint32_t lds_u16(const uint8_t *s)
 {
@@ -126,35 +101,25 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
 __device__ __forceinline__ int tok_of_row(int r) { return (r & 1) * 4 + (r >> 1); }
 __device__ __forceinline__ int row_of_tok(int t) { return (t >> 3) * 8 + (t & 3) * 2 + ((t >> 2) & 1); }
 
-struct Seq {
-    int q0, nq, first_pos, lo, hi, tiles, blocks;
+// How a sequence's work is cut: blocks of 8 NT query columns, tiles of kChunk
+// keys.  Sequences of more than p.few columns are left to the other kernel.
+struct Cut {
+    int blocks, tiles;
 };
 
-// Sequence b's queries and the keys they can see, in chunks from lo.
 template <int NT>
-__device__ __forceinline__ Seq load_seq(const PagedAttnParams &p, int b)
+__device__ __forceinline__ Cut cut(const PagedAttnParams &p, const Seq &s)
 {
-    Seq s;
-    if (p.q_starts != nullptr) {
-        const int a = ld_s32(p.q_starts + b), z = ld_s32(p.q_starts + b + 1);
-        s.q0 = min(max(a, 0), (int)p.n_tokens);
-        s.nq = min(max(z, s.q0), (int)p.n_tokens) - s.q0;
-    } else {
-        s.q0 = b;
-        s.nq = 1;
-    }
-    s.hi = min(max(ld_s32(p.kv_lens + b), 0), p.max_keys);
-    s.first_pos = s.hi - s.nq;
-    s.lo = p.window > 0 ? max(0, s.first_pos - p.window + 1) & ~15 : 0;
-    s.tiles = s.hi > s.lo ? (s.hi - s.lo + kChunk - 1) / kChunk : 1;
-    s.blocks = (s.nq * p.per + 8 * NT - 1) / (8 * NT);
-    return s;
+    const int cols = s.nq * p.per;
+    return Cut{cols > p.few ? 0 : (cols + 8 * NT - 1) / (8 * NT),
+               s.hi > s.lo ? (s.hi - s.lo + kChunk - 1) / kChunk : 1};
 }
 
 template <int NT>
 __device__ __forceinline__ int64_t seq_units(const PagedAttnParams &p, const Seq &s)
 {
-    return (int64_t)p.hk * s.blocks * s.tiles;
+    const Cut c = cut<NT>(p, s);
+    return (int64_t)p.hk * c.blocks * c.tiles;
 }
 
 // Stores 8 NT columns' results: out (and lse) of column col from its sums.
@@ -164,14 +129,14 @@ __device__ __forceinline__ void store_out(const PagedAttnParams &p, const Seq &s
 {
     const int i = col / p.per, h = head * p.per + col % p.per;
     const int64_t row = ((int64_t)(s.q0 + i) * p.hq + h);
-    const float inv = l > 0.0f ? 1.0f / (l * ld_f32(p.v_gs)) : (l == 0.0f ? 0.0f : l);
+    const float inv = out_factor(p, l);
     uint8_t *dst = static_cast<uint8_t *>(p.out) + (row * 128 + d0) * 2;
 #pragma unroll
     for (int k = 0; k < VALS; k += 4)
         *reinterpret_cast<uint2 *>(dst + 2 * k) =
             make_uint2(DT::pack(v[k] * inv, v[k + 1] * inv), DT::pack(v[k + 2] * inv, v[k + 3] * inv));
     if (p.lse != nullptr && d0 == 0)
-        p.lse[row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+        p.lse[row] = lse_of(m, l);
 }
 
 template <typename DT, int NT>
@@ -197,7 +162,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
     const int per_thread = (p.n_seqs + kThreads - 1) / kThreads;
     const int b0 = min(p.n_seqs, (int)threadIdx.x * per_thread), b1 = min(p.n_seqs, b0 + per_thread);
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b) mine += seq_units<NT>(p, load_seq<NT>(p, b));
+    for (int b = b0; b < b1; ++b) mine += seq_units<NT>(p, load_seq(p, b));
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -220,7 +185,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
         int64_t rem = u - (upto - mine);
         int b = b0;
         for (;; ++b) {
-            const int64_t w = seq_units<NT>(p, load_seq<NT>(p, b));
+            const int64_t w = seq_units<NT>(p, load_seq(p, b));
             if (rem < w) break;
             rem -= w;
         }
@@ -244,17 +209,19 @@ paged_attn_split_kernel(const PagedAttnParams p)
     const int vsread = kKVScalesV + c * 8 + g;
     const float inv_kgs = 1.0f / ld_f32(p.k_gs);
 
-    Seq s = load_seq<NT>(p, b);
+    Seq s = load_seq(p, b);
+    Cut ct = cut<NT>(p, s);
     while (u < u_end) {
-        const int64_t all = seq_units<NT>(p, s);
+        const int64_t all = (int64_t)p.hk * ct.blocks * ct.tiles;
         if (rem >= all) {
             rem -= all;
-            s = load_seq<NT>(p, ++b);
+            s = load_seq(p, ++b);
+            ct = cut<NT>(p, s);
             continue;
         }
-        const int item = (int)(rem / s.tiles), tile0 = (int)(rem - (int64_t)item * s.tiles);
-        const int head = item / s.blocks, block = item - head * s.blocks;
-        const int ntile = (int)min((int64_t)(s.tiles - tile0), u_end - u);
+        const int item = (int)(rem / ct.tiles), tile0 = (int)(rem - (int64_t)item * ct.tiles);
+        const int head = item / ct.blocks, block = item - head * ct.blocks;
+        const int ntile = (int)min((int64_t)(ct.tiles - tile0), u_end - u);
         const int col0 = block * 8 * NT, cols = min(8 * NT, s.nq * p.per - col0);
         // keys that the block's columns see: all of [need_lo, need_hi) by every
         // one, nothing from blk_hi on by any
@@ -295,10 +262,9 @@ paged_attn_split_kernel(const PagedAttnParams p)
                 }
                 a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
                 a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
-                // 2^-e and 2^e of the largest element's exponent, kept normal
-                const int e = min(max((int)(__float_as_uint(a) >> 23) - 127, -126), 126);
-                f = __uint_as_float((uint32_t)(127 - e) << 23);
-                back = __uint_as_float((uint32_t)(127 + e) << 23);
+                const float2 pw = row_power(a);
+                f = pw.x;
+                back = pw.y;
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -310,7 +276,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
             const float scale = p.scale * inv_kgs * back;
             cs[nt][0] = __shfl_sync(0xFFFFFFFFu, scale, 8 * c);
             cs[nt][1] = __shfl_sync(0xFFFFFFFFu, scale, 8 * c + 4);
-            m[nt][0] = m[nt][1] = kNone;
+            m[nt][0] = m[nt][1] = kNoMax;
             l[nt][0] = l[nt][1] = 0.0f;
         }
         float o[NT][8][4];
@@ -440,7 +406,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        float top = kNone;
+                        float top = kNoMax;
 #pragma unroll
                         for (int gr = 0; gr < kChunkGroups; ++gr)
 #pragma unroll
@@ -542,7 +508,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
         constexpr int kPerCol = kThreads / (8 * NT), kVals = 128 / kPerCol;
         const int col = threadIdx.x / kPerCol, d0 = (threadIdx.x % kPerCol) * kVals;
         if (col < cols) {
-            float top = kNone, sum = 0.0f, v[kVals] = {};
+            float top = kNoMax, sum = 0.0f, v[kVals] = {};
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[w][col].x);
 #pragma unroll
@@ -554,7 +520,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
 #pragma unroll
                 for (int k = 0; k < kVals; ++k) v[k] = fmaf(f, src[k], v[k]);
             }
-            if (ntile == s.tiles) {
+            if (ntile == ct.tiles) {
                 store_out<DT, kVals>(p, s, head, col0 + col, d0, v, top, sum);
             } else {
                 float *part = parts + (tile0 == 0 ? kPartFloats<NT> : 0);
@@ -566,8 +532,8 @@ paged_attn_split_kernel(const PagedAttnParams p)
                 }
             }
         }
-        if (threadIdx.x == 0 && ntile != s.tiles)
-            info[tile0 == 0] = PartInfo{1, tile0 + ntile == s.tiles, b, head, block};
+        if (threadIdx.x == 0 && ntile != ct.tiles)
+            info[tile0 == 0] = PartInfo{1, tile0 + ntile == ct.tiles, b, head, block};
         __syncthreads();
         u += ntile;
         rem += ntile;
@@ -599,12 +565,12 @@ paged_attn_join_kernel(const PagedAttnParams p, int ctas)
     auto part = [&](int k) {  // the k-th part of the item
         return parts + ((int64_t)(i + k) * 2 + (k == 0)) * kPartFloats<NT>;
     };
-    const Seq s = load_seq<NT>(p, me.seq);
+    const Seq s = load_seq(p, me.seq);
     const int lane = threadIdx.x & 31, d0 = lane * 4;
     for (int col = threadIdx.x >> 5; col < 8 * NT; col += 8) {
         const int at = me.block * 8 * NT + col;
         if (at >= s.nq * p.per) break;
-        float top = kNone;
+        float top = kNoMax;
         for (int k = lane; k < n; k += 32) top = fmaxf(top, part(k)[8 * NT * 128 + col]);
         top = group_max<32>(top);
         float sum = 0.0f, v[4] = {};
@@ -668,8 +634,14 @@ cudaError_t launch_paged_attn(const PagedAttnParams &p, cudaStream_t stream)
     if (e != cudaSuccess) return e;
     // 8 columns hold the queries of a KV head, or 16 do (one pass over the
     // keys instead of two)
-    return (int64_t)p.per * p.max_q <= 8 ? launch_split<DT, 1>(p, dev, stream)
-                                         : launch_split<DT, 2>(p, dev, stream);
+    const int64_t cols = (int64_t)p.per * p.max_q;
+    PagedAttnParams few = p;
+    few.few = INT_MAX;
+    if (cols <= 8) return launch_split<DT, 1>(few, dev, stream);
+    if (p.q_starts == nullptr || cols <= kFewColumns) return launch_split<DT, 2>(few, dev, stream);
+    few.few = kFewColumns;
+    e = launch_split<DT, 2>(few, dev, stream);
+    return e != cudaSuccess ? e : launch_paged_attn_tc<DT>(few, stream);
 }
 
 template cudaError_t launch_paged_attn<BF16>(const PagedAttnParams &, cudaStream_t);

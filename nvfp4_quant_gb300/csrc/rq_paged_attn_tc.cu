@@ -1,0 +1,584 @@
+// rq_paged_attn_tc.cu -- attention over the paged NVFP4 cache for runs of
+// queries (prompts, chunks), on the fifth-generation tensor cores.
+//
+// A CTA takes 256 rows (query, head of the KV head's group) of a sequence as
+// two tiles of 128 and walks the keys in tiles of 128.  Per tile of keys:
+//   S_t = Q_t K^T        tcgen05.mma, both operands in shared memory,
+//   P_t = 2^(S_t c - m)  a thread a row, from and to tensor memory (the fp16 P
+//                        over S's own columns),
+//   O_t += P_t V         tcgen05.mma, P from tensor memory, V from shared,
+// with S and O of both tiles in all 512 tensor-memory columns.  Roles:
+//   warps 0-3, 4-7   the rows of tile 0, tile 1: softmax, and the last step
+//   warps 8-11       a token each: codes from global memory (one tile ahead in
+//                    registers), decoded to fp16 rows in shared memory
+//   warp 12          issues the products: PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1),
+//                    so that one tile's softmax runs under the other's products
+// m follows a row's maximum only when a score exceeds it by 8 (P below 2^8);
+// then the row's O is rescaled in tensor memory, after the product before.
+//
+// What bounds it: 4 * 128 flops a visible pair on the tensor cores.  The
+// operands of a 128 x 128 x 16 product are 8 KB of shared memory in its 64
+// clocks (4 KB with P in tensor memory), the decoded tile another 32 bytes a
+// clock, and the exponentials need half the time of the products.
+//
+// Every wait has a time limit (kWaitNs): past it the CTA gives up, writes NaN
+// and leaves, tensor memory freed.  No valid call meets it.
+#include "rq_paged_attn.cuh"
+
+#include <atomic>
+#include <type_traits>
+
+namespace rq {
+
+namespace {
+
+constexpr int kD = 128, kTile = 128, kRows = 2 * kTile;
+constexpr int kThreads = 13 * 32;
+constexpr uint32_t kTileBytes = kTile * kD * 2;  // 32 KB
+// shared memory (from a 1024-byte boundary): Q0 Q1 K[2] V[2], then the small part
+constexpr uint32_t kQ = 0, kK = 2 * kTileBytes, kV = kK + 2 * kTileBytes, kSmall = kV + 2 * kTileBytes;
+constexpr unsigned long long kWaitNs = 1000000000ull;
+
+struct Small {
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2], drained;
+    uint32_t seen[4][4];  // tile j's readable tokens, ring of 4
+    uint32_t tmem;
+    int failed;
+    int seq, block;
+    int64_t scan[13];
+};
+constexpr size_t kSmemBytes = 1024 + kSmall + sizeof(Small);
+
+// tensor memory columns: S0 S1 O0 O1
+constexpr uint32_t kColS = 0, kColO = 256;
+
+// kind::f16 instruction descriptor: fp32 accumulator, fp16 operands, M = 128,
+// N = 128; bit 16: B is N-major (V).
+constexpr uint32_t kIdescQK = (1u << 4) | ((128u / 8) << 17) | ((128u / 16) << 24);
+constexpr uint32_t kIdescPV = kIdescQK | (1u << 16);
+
+// Shared-memory operand descriptor, 128-byte swizzle (rows of 64 fp16, 8 rows
+// a kilobyte): K-major operands step 1 KB every 8 rows; N-major ones (V, rows
+// are keys) 1 KB every 8 keys and 16 KB from channels 0-63 to 64-127.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFF) | ((uint64_t)(leading >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 :: "r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void async_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 32 columns of the warp's 32 rows; the values are there after tm_wait_ld,
+// which takes them as operands so that no use moves above it.
+__device__ __forceinline__ void tm_load32(uint32_t addr, uint32_t (&v)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
+          "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]),
+          "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]),
+          "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tm_wait_ld(uint32_t (&v)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                   "+r"(v[15]), "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]),
+                   "+r"(v[22]), "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]),
+                   "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
+                 :: "memory");
+}
+__device__ __forceinline__ void tm_store32(uint32_t addr, const uint32_t (&v)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        :: "r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+           "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
+           "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+           "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
+__device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16};"
+        :: "r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+           "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(smem_addr(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ unsigned long long now_ns()
+{
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// Waits until the barrier's phase of the given parity is over; gives up after
+// kWaitNs, or when another role of the CTA has (false).
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *failed)
+{
+    unsigned long long start = 0;
+    for (uint32_t n = 0;; ++n) {
+        uint32_t done;
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                     : "=r"(done) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+        if (done) return true;
+        if ((n & 63) == 63) {
+            if (*failed) return false;
+            const unsigned long long t = now_ns();
+            if (start == 0) start = t;
+            if (t - start > kWaitNs) {
+                *failed = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// The same for a whole warp: every lane gets one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *failed)
+{
+    return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, failed));
+}
+
+// Byte of chunk c (8 channels, 0-15) of row r in a 32 KB operand tile.
+__device__ __forceinline__ uint32_t tile_at(int r, int c)
+{
+    return (uint32_t)(c >> 3) * (kTileBytes / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// Row tiles of the sequence for this kernel.
+__device__ __forceinline__ int row_blocks(const PagedAttnParams &p, const Seq &s)
+{
+    const int rows = s.nq * p.per;
+    return rows > p.few ? (rows + kRows - 1) / kRows : 0;
+}
+
+// A key or value row of a tile: 64 bytes of codes and 8 scales in registers.
+struct Row {
+    uint4 c[4];
+    uint2 f;
+};
+
+__device__ __forceinline__ void load_row(Row &r, const uint8_t *codes, const uint8_t *scales)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.c[i] = ld_keep16(codes + 16 * i);
+    asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(r.f.x), "=r"(r.f.y) : "l"(scales));
+}
+
+__device__ __forceinline__ void decode_row(const Row &r, uint8_t *tile, int row)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {r.c[i].x, r.c[i].y, r.c[i].z, r.c[i].w};
+        const uint32_t two = e4m3_pair(((i & 2) ? r.f.y : r.f.x) >> ((i & 1) * 16));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t f = __byte_perm(two, two, j < 2 ? 0x1010 : 0x3232);
+            sts16(tile + tile_at(row, 4 * i + j),
+                  make_uint4(FP16::mul2(e2m1_pair<0>(w[j]), f), FP16::mul2(e2m1_pair<1>(w[j]), f),
+                             FP16::mul2(e2m1_pair<2>(w[j]), f), FP16::mul2(e2m1_pair<3>(w[j]), f)));
+        }
+    }
+}
+
+template <typename DT>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_attn_tc_kernel(const PagedAttnParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+    Small &sm = *reinterpret_cast<Small *>(smem + kSmall);
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+    // ---- which rows: CTA x / hk in the order of the sequences' row blocks,
+    // the last (longest) block of a sequence first
+    {
+        const int per_thread = (p.n_seqs + kThreads - 1) / kThreads;
+        const int b0 = min(p.n_seqs, (int)threadIdx.x * per_thread), b1 = min(p.n_seqs, b0 + per_thread);
+        int64_t mine = 0;
+        for (int b = b0; b < b1; ++b) mine += row_blocks(p, load_seq(p, b));
+        int64_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) sm.scan[warp] = upto;
+        if (threadIdx.x == 0) {
+            sm.seq = -1;
+            sm.failed = 0;
+            for (int i = 0; i < 2; ++i) {
+                bar_init(&sm.k_full[i], 4);
+                bar_init(&sm.v_full[i], 4);
+                bar_init(&sm.k_empty[i], 1);
+                bar_init(&sm.v_empty[i], 1);
+                bar_init(&sm.s_full[i], 1);
+                bar_init(&sm.p_full[i], 4);
+                bar_init(&sm.pv_done[i], 1);
+            }
+            bar_init(&sm.drained, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) upto += sm.scan[w];
+        int64_t at = blockIdx.x / p.hk;
+        if (upto - mine <= at && at < upto) {
+            at -= upto - mine;
+            for (int b = b0; b < b1; ++b) {
+                const int n = row_blocks(p, load_seq(p, b));
+                if (at < n) {
+                    sm.seq = b;
+                    sm.block = n - 1 - (int)at;
+                    break;
+                }
+                at -= n;
+            }
+        }
+        __syncthreads();
+        if (sm.seq < 0) return;
+    }
+    const int b = sm.seq, head = blockIdx.x % p.hk;
+    const Seq s = load_seq(p, b);
+    const int row0 = sm.block * kRows, rows = min(kRows, s.nq * p.per - row0);
+    // keys that some row of the block sees: [lo, hi), in n tiles
+    const int i_last = (row0 + rows - 1) / p.per, hi = s.first_pos + i_last + 1;
+    const int lo = p.window > 0 ? max(0, s.first_pos + row0 / p.per - p.window + 1) & ~15 : 0;
+    const int n = hi > lo ? (hi - lo + kTile - 1) / kTile : 0;
+
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
+                     :: "r"(smem_addr(&sm.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // ---- queries: a thread a row, times a power of two for bf16
+    float scale = 0.0f;
+    const int t = warp >> 2, r = threadIdx.x & 127;  // tile and row (warps 0-7)
+    const int row = t * kTile + r;                   // of the block
+    const int query = (row0 + row) / p.per;
+    const int64_t out_row = (int64_t)(s.q0 + query) * p.hq + head * p.per + (row0 + row) % p.per;
+    if (warp < 8) {
+        uint8_t *tile = smem + kQ + t * kTileBytes;
+        const uint8_t *src = static_cast<const uint8_t *>(p.q) +
+                             ((s.q0 + query) * p.q_stride + (int64_t)(head * p.per + (row0 + row) % p.per) * kD) * 2;
+        const bool real = row < rows;
+        float f = 1.0f, back = 1.0f;
+        if (std::is_same<DT, BF16>::value && real) {
+            float a = 0.0f;
+#pragma unroll 4
+            for (int c = 0; c < 16; ++c) {
+                float e[8];
+                unpack8<DT>(ld_keep16(src + 16 * c), e);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) a = fmaxf(a, fabsf(e[k]));
+            }
+            const float2 pw = row_power(a);
+            f = pw.x;
+            back = pw.y;
+        }
+        scale = p.scale * back / ld_f32(p.k_gs);
+#pragma unroll 4
+        for (int c = 0; c < 16; ++c) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (real) v = ld_keep16(src + 16 * c);
+            if (std::is_same<DT, BF16>::value) {
+                float e[8];
+                unpack8<DT>(v, e);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) e[k] *= f;
+                v = pack8<FP16>(e);
+            }
+            sts16(tile + tile_at(r, c), v);
+        }
+        async_proxy_fence();
+    }
+    tm_fence_before();
+    __syncthreads();
+    tm_fence_after();
+    const uint32_t tmem = sm.tmem;
+    volatile int *failed = &sm.failed;
+
+    if (warp == 12) {
+        // ---------------------------------------------------------- products
+        if (lane == 0 && n > 0) {
+            const uint32_t base = smem_addr(smem);
+            bool ok = true;
+            auto qk = [&](int tt, int j) {
+                const uint32_t a = base + kQ + tt * kTileBytes, bk = base + kK + (j & 1) * kTileBytes;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint32_t off = (k >> 2) * (kTileBytes / 2) + (k & 3) * 32;
+                    mma_ss(tmem + kColS + tt * 128, operand(a + off, 16), operand(bk + off, 16), kIdescQK, k > 0);
+                }
+                mma_commit(&sm.s_full[tt]);
+            };
+            ok = bar_wait(&sm.k_full[0], 0, failed);
+            if (ok) {
+                tm_fence_after();
+                qk(0, 0);
+                qk(1, 0);
+                mma_commit(&sm.k_empty[0]);
+            }
+            for (int j = 0; ok && j < n; ++j) {
+                ok = bar_wait(&sm.v_full[j & 1], (j >> 1) & 1, failed);
+                for (int tt = 0; ok && tt < 2; ++tt) {
+                    ok = bar_wait(&sm.p_full[tt], j & 1, failed);
+                    if (!ok) break;
+                    tm_fence_after();
+                    const uint32_t bv = base + kV + (j & 1) * kTileBytes;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_ts(tmem + kColO + tt * 128, tmem + kColS + tt * 128 + k * 8,
+                               operand(bv + k * 2048, kTileBytes / 2), kIdescPV, j > 0 || k > 0);
+                    mma_commit(&sm.pv_done[tt]);
+                    if (tt == 1) mma_commit(&sm.v_empty[j & 1]);
+                    if (j + 1 < n) {
+                        if (tt == 0) {
+                            ok = bar_wait(&sm.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, failed);
+                            if (!ok) break;
+                            tm_fence_after();
+                        }
+                        qk(tt, j + 1);
+                        if (tt == 1) mma_commit(&sm.k_empty[(j + 1) & 1]);
+                    }
+                }
+            }
+            // no product may outlive the operands and the tensor memory, also
+            // when the loop gave up
+            int none = 0;
+            mma_commit(&sm.drained);
+            bar_wait(&sm.drained, 0, &none);
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        // ---------------------------------------------------------- keys and values
+        const int tok = threadIdx.x - 8 * 32;  // of the tile
+        auto find = [&](int j) -> const uint8_t * {  // the token's group
+            const int at = lo + j * kTile + tok;
+            if (j >= n || at >= hi) return nullptr;
+            const int slot = at >> 4, page = slot / p.groups;
+            const int id = ld_s32(p.table + (int64_t)b * p.table_stride + page);
+            if (id < 0 || id >= p.num_pages) return nullptr;
+            return p.pool + (((int64_t)id * p.hk + head) * p.groups + (slot - page * p.groups)) * kKVGroupBytes;
+        };
+        const int in_group = tok & 15;  // lo is a multiple of 16
+        auto load_k = [&](Row &x, const uint8_t *g) {
+            x = Row{};
+            if (g != nullptr) load_row(x, g + kKVCodesK + in_group * 64, g + kKVScalesK + in_group * 8);
+        };
+        auto load_v = [&](Row &x, const uint8_t *g) {
+            x = Row{};
+            if (g != nullptr) load_row(x, g + kKVCodesV + in_group * 64, g + kKVScalesV + in_group * 8);
+        };
+        Row k, v;
+        const uint8_t *g = find(0), *g_next = find(1);
+        load_k(k, g);
+        load_v(v, g);
+        for (int j = 0; j < n; ++j) {
+            const int st = j & 1;
+            if (j >= 2 && !warp_wait(&sm.k_empty[st], ((j >> 1) + 1) & 1, failed)) break;
+            const uint32_t seen = __ballot_sync(0xFFFFFFFFu, g != nullptr);
+            if (lane == 0) sm.seen[j & 3][warp - 8] = seen;
+            decode_row(k, smem + kK + st * kTileBytes, tok);
+            async_proxy_fence();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sm.k_full[st]);
+            load_k(k, g_next);
+            if (j >= 2 && !warp_wait(&sm.v_empty[st], ((j >> 1) + 1) & 1, failed)) break;
+            decode_row(v, smem + kV + st * kTileBytes, tok);
+            async_proxy_fence();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sm.v_full[st]);
+            load_v(v, g_next);
+            g = g_next;
+            g_next = find(j + 2);
+        }
+    } else {
+        // ---------------------------------------------------------- softmax
+        const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's 32 rows
+        const uint32_t s_at = at + kColS + t * 128, o_at = at + kColO + t * 128;
+        const bool real = row < rows;
+        const int row_hi = real ? s.first_pos + query + 1 : 0;               // keys [row_lo, row_hi)
+        const int row_lo = p.window > 0 ? row_hi - p.window : 0;
+        float m = kNoMax, l = 0.0f;
+        for (int j = 0; j < n; ++j) {
+            if (!warp_wait(&sm.s_full[t], j & 1, failed)) break;
+            tm_fence_after();
+            auto visible = [&](int c) {  // of the tile's columns 32 c ..
+                const int first = lo + j * kTile + 32 * c, below = row_hi - first, from = row_lo - first;
+                const uint32_t a = below >= 32 ? ~0u : (below <= 0 ? 0u : (1u << below) - 1u);
+                const uint32_t z = from <= 0 ? 0u : (from >= 32 ? ~0u : (1u << from) - 1u);
+                return a & ~z & sm.seen[j & 3][c];
+            };
+            uint32_t pk[64];
+            float high = kNoMax;
+            float2 sum = make_float2(0.0f, 0.0f);
+            const float2 s2 = make_float2(scale, scale);
+            auto exps = [&](uint32_t (&x)[32], int c, float2 nm) {  // one chunk of P and of the sum
+                const uint32_t vis = visible(c);
+                const bool all = __all_sync(0xFFFFFFFFu, vis == ~0u);
+#pragma unroll
+                for (int k = 0; k < 32; k += 2) {
+                    float2 y = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), s2, nm);
+                    if (!all) {
+                        if (!(vis & (1u << k))) y.x = -INFINITY;
+                        if (!(vis & (2u << k))) y.y = -INFINITY;
+                    }
+                    high = fmaxf(high, fmaxf(y.x, y.y));
+                    y.x = ex2(y.x);
+                    y.y = ex2(y.y);
+                    sum = __fadd2_rn(sum, y);
+                    pk[16 * c + k / 2] = FP16::pack(y.x, y.y);
+                }
+            };
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t x[32];
+                tm_load32(s_at + 32 * c, x);
+                tm_wait_ld(x);
+                exps(x, c, make_float2(-m, -m));
+            }
+            if (__any_sync(0xFFFFFFFFu, high > kRaise)) {
+                // a row's maximum has risen: take it, rescale, and form P again
+                float top = m;
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32];
+                    tm_load32(s_at + 32 * c, x);
+                    tm_wait_ld(x);
+                    const uint32_t vis = visible(c);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (vis & (1u << k)) top = fmaxf(top, __uint_as_float(x[k]) * scale);
+                }
+                const float f = ex2(m - top);
+                m = top;
+                l *= f;
+                if (j > 0) {
+                    if (!warp_wait(&sm.pv_done[t], (j - 1) & 1, failed)) break;
+                    tm_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t x[32];
+                        tm_load32(o_at + 32 * c, x);
+                        tm_wait_ld(x);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
+                        tm_store32(o_at + 32 * c, x);
+                    }
+                }
+                sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t x[32];
+                    tm_load32(s_at + 32 * c, x);
+                    tm_wait_ld(x);
+                    exps(x, c, make_float2(-m, -m));
+                }
+            }
+            l += sum.x + sum.y;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tm_store16(s_at + 16 * c, pk + 16 * c);
+            tm_wait_st();
+            tm_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&sm.p_full[t]);
+        }
+        // ---------------------------------------------------------- last step
+        if (n > 0) {
+            warp_wait(&sm.pv_done[t], (n - 1) & 1, failed);
+            tm_fence_after();
+        }
+        const float inv = *failed ? __uint_as_float(0x7FC00000u) : out_factor(p, l);
+        uint8_t *dst = static_cast<uint8_t *>(p.out) + out_row * (kD * 2);
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+            uint32_t x[32] = {};
+            if (n > 0) {
+                tm_load32(o_at + 32 * c, x);
+                tm_wait_ld(x);
+            }
+            if (real) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    float e[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) e[i] = l == 0.0f && !*failed ? 0.0f : __uint_as_float(x[k + i]) * inv;
+                    st16(dst + 64 * c + 2 * k, pack8<DT>(e));
+                }
+            }
+        }
+        if (real && p.lse != nullptr) p.lse[out_row] = *failed ? __uint_as_float(0x7FC00000u) : lse_of(m, l);
+    }
+    // ---------------------------------------------------------------- leave
+    tm_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tm_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" :: "r"(tmem) : "memory");
+    }
+}
+
+}  // namespace
+
+template <typename DT>
+cudaError_t launch_paged_attn_tc(const PagedAttnParams &p, cudaStream_t stream)
+{
+    static std::atomic<int> ready[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    auto kern = paged_attn_tc_kernel<DT>;
+    if (dev >= 64 || !ready[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready[dev].store(1, std::memory_order_relaxed);
+    }
+    // every sequence has a part of a row block at most beside its full ones
+    const int64_t rows = p.n_tokens * p.per;
+    const int64_t blocks = rows / kRows + (rows / (p.few + 1) < p.n_seqs ? rows / (p.few + 1) : p.n_seqs);
+    if (blocks * p.hk > INT32_MAX) return cudaErrorInvalidConfiguration;
+    return blocks > 0 ? launch_pdl(kern, (unsigned)(blocks * p.hk), kThreads, kSmemBytes, stream, p) : cudaSuccess;
+}
+
+template cudaError_t launch_paged_attn_tc<BF16>(const PagedAttnParams &, cudaStream_t);
+template cudaError_t launch_paged_attn_tc<FP16>(const PagedAttnParams &, cudaStream_t);
+
+}  // namespace rq
