@@ -13,8 +13,10 @@
 //                    registers), decoded to fp16 rows in shared memory
 //   warp 12          issues the products: PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1),
 //                    so that one tile's softmax runs under the other's products
-// m follows a row's maximum only when a score exceeds it by 8 (P below 2^8);
-// then the row's O is rescaled in tensor memory, after the product before.
+// m is the row's maximum when it was last looked at.  That is when a tile's sum
+// of P passes kPMax (so no P exceeds it, and fp16 holds them all): the row's O
+// is then rescaled in tensor memory, after the product before.  Between, no
+// maximum is formed.
 //
 // What bounds it: 4 * 128 flops a visible pair on the tensor cores.  The
 // operands of a 128 x 128 x 16 product are 8 KB of shared memory in its 64
@@ -37,6 +39,7 @@ constexpr int kThreads = 13 * 32;
 constexpr uint32_t kTileBytes = kTile * kD * 2;  // 32 KB
 // shared memory (from a 1024-byte boundary): Q0 Q1 K[2] V[2], then the small part
 constexpr uint32_t kQ = 0, kK = 2 * kTileBytes, kV = kK + 2 * kTileBytes, kSmall = kV + 2 * kTileBytes;
+constexpr float kPMax = 32768.0f;  // below fp16's largest value
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
 struct Small {
@@ -167,6 +170,13 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatil
             }
         }
     }
+}
+
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+    return one != 0;
 }
 
 // The same for a whole warp: every lane gets one answer.
@@ -337,56 +347,61 @@ paged_attn_tc_kernel(const PagedAttnParams p)
 
     if (warp == 12) {
         // ---------------------------------------------------------- products
-        if (lane == 0 && n > 0) {
-            const uint32_t base = smem_addr(smem);
-            bool ok = true;
-            auto qk = [&](int tt, int j) {
-                const uint32_t a = base + kQ + tt * kTileBytes, bk = base + kK + (j & 1) * kTileBytes;
+        // The whole warp walks the loop, one elected lane issues: addresses
+        // and descriptors then stay in uniform registers (a loop in one lane
+        // alone spent 70 clocks a product moving them there, more than the
+        // product takes: 587 us against 474 for 8192 tokens of 32 heads).
+        const uint32_t base = smem_addr(smem);
+        const uint64_t dq = operand(base + kQ, 16), dk = operand(base + kK, 16);
+        const uint64_t dv = operand(base + kV, kTileBytes / 2);
+        const bool lead = elect_one();
+        auto qk = [&](int tt, int j) {
+            const uint64_t a = dq + tt * (kTileBytes >> 4), bk = dk + (j & 1) * (kTileBytes >> 4);
+            if (lead) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const uint32_t off = (k >> 2) * (kTileBytes / 2) + (k & 3) * 32;
-                    mma_ss(tmem + kColS + tt * 128, operand(a + off, 16), operand(bk + off, 16), kIdescQK, k > 0);
+                    const uint32_t off = ((k >> 2) * (kTileBytes / 2) + (k & 3) * 32) >> 4;
+                    mma_ss(tmem + kColS + tt * 128, a + off, bk + off, kIdescQK, k > 0);
                 }
                 mma_commit(&sm.s_full[tt]);
-            };
-            ok = bar_wait(&sm.k_full[0], 0, failed);
-            if (ok) {
-                tm_fence_after();
-                qk(0, 0);
-                qk(1, 0);
-                mma_commit(&sm.k_empty[0]);
+                if (tt == 1) mma_commit(&sm.k_empty[j & 1]);
             }
-            for (int j = 0; ok && j < n; ++j) {
-                ok = bar_wait(&sm.v_full[j & 1], (j >> 1) & 1, failed);
-                for (int tt = 0; ok && tt < 2; ++tt) {
-                    ok = bar_wait(&sm.p_full[tt], j & 1, failed);
-                    if (!ok) break;
-                    tm_fence_after();
-                    const uint32_t bv = base + kV + (j & 1) * kTileBytes;
+        };
+        bool ok = n > 0 && warp_wait(&sm.k_full[0], 0, failed);
+        if (ok) {
+            tm_fence_after();
+            qk(0, 0);
+            qk(1, 0);
+        }
+        for (int j = 0; ok && j < n; ++j) {
+            ok = warp_wait(&sm.v_full[j & 1], (j >> 1) & 1, failed);
+            const uint64_t bv = dv + (j & 1) * (kTileBytes >> 4);
+#pragma unroll
+            for (int tt = 0; tt < 2; ++tt) {
+                if (!ok || !(ok = warp_wait(&sm.p_full[tt], j & 1, failed))) break;
+                tm_fence_after();
+                if (lead) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_ts(tmem + kColO + tt * 128, tmem + kColS + tt * 128 + k * 8,
-                               operand(bv + k * 2048, kTileBytes / 2), kIdescPV, j > 0 || k > 0);
+                        mma_ts(tmem + kColO + tt * 128, tmem + kColS + tt * 128 + k * 8, bv + k * (2048 >> 4),
+                               kIdescPV, j > 0 || k > 0);
                     mma_commit(&sm.pv_done[tt]);
                     if (tt == 1) mma_commit(&sm.v_empty[j & 1]);
-                    if (j + 1 < n) {
-                        if (tt == 0) {
-                            ok = bar_wait(&sm.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, failed);
-                            if (!ok) break;
-                            tm_fence_after();
-                        }
-                        qk(tt, j + 1);
-                        if (tt == 1) mma_commit(&sm.k_empty[(j + 1) & 1]);
+                }
+                if (j + 1 < n) {
+                    if (tt == 0) {
+                        if (!(ok = warp_wait(&sm.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, failed))) break;
+                        tm_fence_after();
                     }
+                    qk(tt, j + 1);
                 }
             }
-            // no product may outlive the operands and the tensor memory, also
-            // when the loop gave up
-            int none = 0;
-            mma_commit(&sm.drained);
-            bar_wait(&sm.drained, 0, &none);
         }
-        __syncwarp();
+        // no product may outlive the operands and the tensor memory, also
+        // when the loop gave up
+        int none = 0;
+        if (lead) mma_commit(&sm.drained);
+        warp_wait(&sm.drained, 0, &none);
     } else if (warp >= 8) {
         // ---------------------------------------------------------- keys and values
         const int tok = threadIdx.x - 8 * 32;  // of the tile
@@ -448,34 +463,42 @@ paged_attn_tc_kernel(const PagedAttnParams p)
                 return a & ~z & sm.seen[j & 3][c];
             };
             uint32_t pk[64];
-            float high = kNoMax;
             float2 sum = make_float2(0.0f, 0.0f);
             const float2 s2 = make_float2(scale, scale);
-            auto exps = [&](uint32_t (&x)[32], int c, float2 nm) {  // one chunk of P and of the sum
+            auto exps = [&](uint32_t (&x)[32], int c) {  // one chunk of P and of the sum
                 const uint32_t vis = visible(c);
-                const bool all = __all_sync(0xFFFFFFFFu, vis == ~0u);
+                if (__any_sync(0xFFFFFFFFu, vis != ~0u)) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (!(vis & (1u << k))) x[k] = 0xFF800000u;  // -inf
+                }
+                const float2 nm = make_float2(-m, -m);
 #pragma unroll
                 for (int k = 0; k < 32; k += 2) {
                     float2 y = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), s2, nm);
-                    if (!all) {
-                        if (!(vis & (1u << k))) y.x = -INFINITY;
-                        if (!(vis & (2u << k))) y.y = -INFINITY;
-                    }
-                    high = fmaxf(high, fmaxf(y.x, y.y));
                     y.x = ex2(y.x);
                     y.y = ex2(y.y);
                     sum = __fadd2_rn(sum, y);
                     pk[16 * c + k / 2] = FP16::pack(y.x, y.y);
                 }
             };
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t x[32];
-                tm_load32(s_at + 32 * c, x);
-                tm_wait_ld(x);
-                exps(x, c, make_float2(-m, -m));
-            }
-            if (__any_sync(0xFFFFFFFFu, high > kRaise)) {
+            auto all_exps = [&]() {  // the next chunk's scores arrive meanwhile
+                uint32_t x0[32], x1[32];
+                tm_load32(s_at, x0);
+                tm_wait_ld(x0);
+                tm_load32(s_at + 32, x1);
+                exps(x0, 0);
+                tm_wait_ld(x1);
+                tm_load32(s_at + 64, x0);
+                exps(x1, 1);
+                tm_wait_ld(x0);
+                tm_load32(s_at + 96, x1);
+                exps(x0, 2);
+                tm_wait_ld(x1);
+                exps(x1, 3);
+            };
+            all_exps();
+            if (__any_sync(0xFFFFFFFFu, sum.x + sum.y > kPMax)) {
                 // a row's maximum has risen: take it, rescale, and form P again
                 float top = m;
 #pragma unroll 1
@@ -505,13 +528,7 @@ paged_attn_tc_kernel(const PagedAttnParams p)
                     }
                 }
                 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t x[32];
-                    tm_load32(s_at + 32 * c, x);
-                    tm_wait_ld(x);
-                    exps(x, c, make_float2(-m, -m));
-                }
+                all_exps();
             }
             l += sum.x + sum.y;
 #pragma unroll
