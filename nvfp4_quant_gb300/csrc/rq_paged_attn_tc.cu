@@ -374,7 +374,8 @@ paged_attn_tc_kernel(const PagedAttnParams p)
             qk(1, 0);
         }
         for (int j = 0; ok && j < n; ++j) {
-            ok = warp_wait(&sm.v_full[j & 1], (j >> 1) & 1, failed);
+            ok = warp_wait(&sm.v_full[j & 1], (j >> 1) & 1, failed) &&
+                 (j + 1 == n || warp_wait(&sm.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, failed));
             const uint64_t bv = dv + (j & 1) * (kTileBytes >> 4);
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
@@ -388,13 +389,7 @@ paged_attn_tc_kernel(const PagedAttnParams p)
                     mma_commit(&sm.pv_done[tt]);
                     if (tt == 1) mma_commit(&sm.v_empty[j & 1]);
                 }
-                if (j + 1 < n) {
-                    if (tt == 0) {
-                        if (!(ok = warp_wait(&sm.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, failed))) break;
-                        tm_fence_after();
-                    }
-                    qk(tt, j + 1);
-                }
+                if (j + 1 < n) qk(tt, j + 1);
             }
         }
         // no product may outlive the operands and the tensor memory, also
@@ -463,7 +458,7 @@ paged_attn_tc_kernel(const PagedAttnParams p)
                 return a & ~z & sm.seen[j & 3][c];
             };
             uint32_t pk[64];
-            float2 sum = make_float2(0.0f, 0.0f);
+            float sum[4] = {};
             const float2 s2 = make_float2(scale, scale);
             auto exps = [&](uint32_t (&x)[32], int c) {  // one chunk of P and of the sum
                 const uint32_t vis = visible(c);
@@ -472,14 +467,26 @@ paged_attn_tc_kernel(const PagedAttnParams p)
                     for (int k = 0; k < 32; ++k)
                         if (!(vis & (1u << k))) x[k] = 0xFF800000u;  // -inf
                 }
+                // 16 at a time: the exponentials first, then what uses them
+                // (this file is compiled with little instruction scheduling,
+                // so that they stay apart: the scheduler's own order put each
+                // use behind its exponential and took 14 clocks an element of
+                // a lone warp where this takes 6.6)
                 const float2 nm = make_float2(-m, -m);
 #pragma unroll
-                for (int k = 0; k < 32; k += 2) {
-                    float2 y = __ffma2_rn(make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), s2, nm);
-                    y.x = ex2(y.x);
-                    y.y = ex2(y.y);
-                    sum = __fadd2_rn(sum, y);
-                    pk[16 * c + k / 2] = FP16::pack(y.x, y.y);
+                for (int k0 = 0; k0 < 32; k0 += 16) {
+                    float y[16];
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) {
+                        const float2 z = __ffma2_rn(
+                            make_float2(__uint_as_float(x[k0 + k]), __uint_as_float(x[k0 + k + 1])), s2, nm);
+                        y[k] = ex2(z.x);
+                        y[k + 1] = ex2(z.y);
+                    }
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) sum[k & 3] += y[k];
+#pragma unroll
+                    for (int k = 0; k < 16; k += 2) pk[16 * c + (k0 + k) / 2] = FP16::pack(y[k], y[k + 1]);
                 }
             };
             auto all_exps = [&]() {  // the next chunk's scores arrive meanwhile
@@ -498,7 +505,7 @@ paged_attn_tc_kernel(const PagedAttnParams p)
                 exps(x1, 3);
             };
             all_exps();
-            if (__any_sync(0xFFFFFFFFu, sum.x + sum.y > kPMax)) {
+            if (__any_sync(0xFFFFFFFFu, sum[0] + sum[1] + sum[2] + sum[3] > kPMax)) {
                 // a row's maximum has risen: take it, rescale, and form P again
                 float top = m;
 #pragma unroll 1
@@ -527,10 +534,10 @@ paged_attn_tc_kernel(const PagedAttnParams p)
                         tm_store32(o_at + 32 * c, x);
                     }
                 }
-                sum = make_float2(0.0f, 0.0f);
+                sum[0] = sum[1] = sum[2] = sum[3] = 0.0f;
                 all_exps();
             }
-            l += sum.x + sum.y;
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) tm_store16(s_at + 16 * c, pk + 16 * c);
             tm_wait_st();
