@@ -3,10 +3,11 @@
 // split over CTAs, each CTA's share over its warps, and the parts joined.
 //
 // Mathematics.  With x_j = scale log2(e) q . k_j, a part of the keys gives
-//   m >= max x_j - 8,  l = sum 2^(x_j - m),  O = sum 2^(x_j - m) v_j
-// and parts join by (m, l, O) -> sum of 2^(m_i - m) (l_i, O_i).  m is moved
-// only when some x exceeds it by more than 8 (the fp16 probabilities then stay
-// below 2^8), so most tiles need no reduction over lanes.
+//   l = sum 2^(x_j - m),  O = sum 2^(x_j - m) v_j
+// for any m, and parts join by (m, l, O) -> sum of 2^(m_i - m) (l_i, O_i).  m is
+// a maximum when it was last looked at: when a step's sum of exponentials
+// passes kPMax (so that fp16 holds each of them).  Most steps need no maximum
+// and no reduction over lanes.
 //
 // What bounds it: 144 bytes a key and KV head have to come from HBM; at 6.8
 // TB/s an SM gets one every 6.1 clocks.  The products run on mma.sync with
@@ -60,23 +61,42 @@ struct PartInfo {
 
 constexpr size_t kInfoBytes = ((size_t)kMaxCtas * 2 * sizeof(PartInfo) + 15) / 16 * 16;
 
-__device__ __forceinline__ uint32_t lds_u16(const uint8_t *s)
+// Shared memory at a 32-bit address plus a constant (an address that goes
+// through a generic pointer costs three more instructions a load).
+template <int OFF>
+__device__ __forceinline__ uint4 lds16_at(uint32_t a)
 {
-    uint16_t v;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(smem_addr(s)) : "memory");
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4 + %5];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a), "n"(OFF) : "memory");
     return v;
 }
-__device__ __forceinline__ uint32_t lds_u8(const uint8_t *s)
-{
-    uint32_t v;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(smem_addr(s)) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint2 lds8(const uint8_t *s)
+template <int OFF>
+__device__ __forceinline__ uint2 lds8_at(uint32_t a)
 {
     uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(smem_addr(s)) : "memory");
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2 + %3];" : "=r"(v.x), "=r"(v.y) : "r"(a), "n"(OFF) : "memory");
     return v;
+}
+template <int OFF>
+__device__ __forceinline__ uint32_t lds2_at(uint32_t a)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=h"(v) : "r"(a), "n"(OFF) : "memory");
+    return v;
+}
+template <int OFF>
+__device__ __forceinline__ uint32_t lds1_at(uint32_t a)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1 + %2];" : "=r"(v) : "r"(a), "n"(OFF) : "memory");
+    return v;
+}
+template <int DST, int SRC>
+__device__ __forceinline__ void cp16_at(uint32_t dst, const uint8_t *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0 + %1], [%2 + %3], 16;"
+                 :: "r"(dst), "n"(DST), "l"(src), "n"(SRC) : "memory");
 }
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -198,15 +218,17 @@ paged_attn_split_kernel(const PagedAttnParams p)
     int b = start_seq;
     int64_t rem = start_rem;
 
-    uint8_t *ring = smem + warp * (kStages * kChunkBytes);
+    const uint32_t ring = smem_addr(smem) + warp * (kStages * kChunkBytes);
+    float *warp_o = reinterpret_cast<float *>(smem + warp * (kStages * kChunkBytes));
     // where the lane's 16-byte pieces of a group go (the fifth: lanes 0-15)
-    const int kdst = row_of_tok(lane >> 2) * 64 + (lane & 3) * 16;  // + 512: tokens 8-15
-    const int vdst = kKVCodesV + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 1) * 2) * 16);
+    const uint32_t kdst = ring + row_of_tok(lane >> 2) * 64 + (lane & 3) * 16;  // + 512: tokens 8-15
+    const uint32_t vdst = ring + kKVCodesV + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 1) * 2) * 16);
+    const uint32_t fdst = ring + kKVScalesK + lane * 16;
     // where it reads them
-    const int kread = g * 64 + c * 16;
-    const int vread = kKVCodesV + c * 64 + (((g >> 1) ^ ((c >> 1) & 1) * 2) * 16) + (g & 1) * 8;
-    const int ksread = kKVScalesK + tok_of_row(g) * 8 + 2 * c;
-    const int vsread = kKVScalesV + c * 8 + g;
+    const uint32_t kread = ring + g * 64 + c * 16;
+    const uint32_t vread = ring + kKVCodesV + c * 64 + (((g >> 1) ^ ((c >> 1) & 1) * 2) * 16) + (g & 1) * 8;
+    const uint32_t ksread = ring + kKVScalesK + tok_of_row(g) * 8 + 2 * c;
+    const uint32_t vsread = ring + kKVScalesV + c * 8 + g;
     const float inv_kgs = 1.0f / ld_f32(p.k_gs);
 
     Seq s = load_seq(p, b);
@@ -234,6 +256,40 @@ paged_attn_split_kernel(const PagedAttnParams p)
         const int chunks = t1 > t0 + warp * kChunk
                                ? (t1 - t0 - warp * kChunk + kWarps * kChunk - 1) / (kWarps * kChunk)
                                : 0;  // of this warp
+
+        // ---- groups of the warp's chunks, 16 chunks at a time: lane 2 i + j
+        // holds where group j of chunk i lies in the cache (-1: nowhere)
+        auto find = [&](int batch) {
+            const int token = t0 + (warp + kWarps * (batch * 16 + (lane >> 1))) * kChunk + (lane & 1) * 16;
+            int at = -1;
+            if (token < t1) {
+                const int slot = token >> 4, page = slot / p.groups;
+                const int id = ld_s32(p.table + (int64_t)b * p.table_stride + page);
+                if (id >= 0 && id < p.num_pages)
+                    at = (int)(((int64_t)id * p.hk + head) * p.groups + (slot - page * p.groups));
+            }
+            return at;
+        };
+        auto fetch = [&](int i, int from, uint32_t stage) {  // starts the copies of chunk i
+#pragma unroll
+            for (int gr = 0; gr < kChunkGroups; ++gr) {
+                const int at = __shfl_sync(0xFFFFFFFFu, from, (i & 15) * 2 + gr);
+                if (at >= 0 && i < chunks) {
+                    const uint8_t *src = p.pool + (int64_t)at * kKVGroupBytes + lane * 16;
+                    const uint32_t d = stage + gr * kKVGroupBytes;
+                    cp16_at<0, 0>(d + kdst, src);
+                    cp16_at<512, 512>(d + kdst, src);
+                    cp16_at<0, 1024>(d + vdst, src);
+                    cp16_at<512, 1536>(d + vdst, src);
+                    if (lane < 16) cp16_at<0, 2048>(d + fdst, src);
+                }
+            }
+            cp_async_commit();
+        };
+        int near = find(0), far = find(1);
+        for (int i = 0; i < kStages - 1; ++i) fetch(i, near, i * kChunkBytes);
+        uint32_t near_ok = __ballot_sync(0xFFFFFFFFu, near >= 0);
+        uint32_t stage = 0, filled = (kStages - 1) * kChunkBytes;  // of chunk it, of the next to fetch
 
         // ---- queries: columns nt * 8 + g, channels 32 c .. + 31, as the B
         // operand; each row by a power of two so that fp16 holds it
@@ -273,7 +329,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) qf[nt][4 * k + j] = FP16::pack(e[2 * j] * f, e[2 * j + 1] * f);
             }
-            const float scale = p.scale * inv_kgs * back;
+            const float scale = fmaxf(p.scale * inv_kgs * back, kLeastScale);
             cs[nt][0] = __shfl_sync(0xFFFFFFFFu, scale, 8 * c);
             cs[nt][1] = __shfl_sync(0xFFFFFFFFu, scale, 8 * c + 4);
             m[nt][0] = m[nt][1] = kNoMax;
@@ -287,65 +343,27 @@ paged_attn_split_kernel(const PagedAttnParams p)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.0f;
 
-        // ---- groups of the warp's chunks, 16 chunks at a time: lane 2 i + j
-        // holds where group j of chunk i lies in the cache (-1: nowhere)
-        auto find = [&](int batch) {
-            const int token = t0 + (warp + kWarps * (batch * 16 + (lane >> 1))) * kChunk + (lane & 1) * 16;
-            int at = -1;
-            if (token < t1) {
-                const int slot = token >> 4, page = slot / p.groups;
-                const int id = ld_s32(p.table + (int64_t)b * p.table_stride + page);
-                if (id >= 0 && id < p.num_pages)
-                    at = (int)(((int64_t)id * p.hk + head) * p.groups + (slot - page * p.groups));
-            }
-            return at;
-        };
-        int near = find(0), far = find(1);
-        auto fetch = [&](int i, int cur_batch) {  // starts the copies of chunk i
-            const int from = (i >> 4) == cur_batch ? near : far;
-            uint8_t *to = ring + (i % kStages) * kChunkBytes;
-#pragma unroll
-            for (int gr = 0; gr < kChunkGroups; ++gr) {
-                const int at = __shfl_sync(0xFFFFFFFFu, from, (i & 15) * 2 + gr);
-                if (at >= 0 && i < chunks) {
-                    const uint8_t *src = p.pool + (int64_t)at * kKVGroupBytes + lane * 16;
-                    uint8_t *d = to + gr * kKVGroupBytes;
-                    cp_async16(d + kdst, src);
-                    cp_async16(d + kdst + 512, src + 512);
-                    cp_async16(d + vdst, src + 1024);
-                    cp_async16(d + vdst + 512, src + 1536);
-                    if (lane < 16) cp_async16(d + 2048 + lane * 16, src + 2048);
-                }
-            }
-            cp_async_commit();
-        };
-        for (int i = 0; i < kStages - 1; ++i) fetch(i, 0);
-
         for (int it = 0; it < chunks; ++it) {
             cp_async_wait<kStages - 2>();
             __syncwarp();  // everyone's copies have landed; everyone is done with the stage before
             if (it > 0 && (it & 15) == 0) {
                 near = far;
                 far = find((it >> 4) + 1);
+                near_ok = __ballot_sync(0xFFFFFFFFu, near >= 0);
             }
-            fetch(it + kStages - 1, it >> 4);
-            const uint8_t *stage = ring + (it % kStages) * kChunkBytes;
+            fetch(it + kStages - 1, (it & 15) + kStages - 1 < 16 ? near : far, filled);
             const int tok0 = t0 + (warp + kWarps * it) * kChunk;
-            bool here[kChunkGroups], full = tok0 >= need_lo && tok0 + kChunk <= need_hi;
-#pragma unroll
-            for (int gr = 0; gr < kChunkGroups; ++gr) {
-                here[gr] = __shfl_sync(0xFFFFFFFFu, near, (it & 15) * 2 + gr) >= 0;
-                full &= here[gr];
-            }
+            const uint32_t here = near_ok >> ((it & 15) * 2);  // bit gr: the group is readable
+            const bool full = tok0 >= need_lo && tok0 + kChunk <= need_hi && (here & 3u) == 3u;
 
             // ---- S^T = K Q^T
             float x[kChunkGroups][NT][4];
 #pragma unroll
             for (int gr = 0; gr < kChunkGroups; ++gr) {
-                const uint8_t *base = stage + gr * kKVGroupBytes;
-                const uint4 ka = lds16(base + kread), kb = lds16(base + kread + 512);
-                const uint32_t sa = e4m3_pair(lds_u16(base + ksread));
-                const uint32_t sb = e4m3_pair(lds_u16(base + ksread + 64));
+                const uint32_t base = stage + gr * kKVGroupBytes;
+                const uint4 ka = lds16_at<0>(base + kread), kb = lds16_at<512>(base + kread);
+                const uint32_t sa = e4m3_pair(lds2_at<0>(base + ksread));
+                const uint32_t sb = e4m3_pair(lds2_at<64>(base + ksread));
                 const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -383,27 +401,41 @@ paged_attn_split_kernel(const PagedAttnParams p)
                             const int t = tok0 + gr * 16 + tok_of_row(g) + (e >> 1) * 8;
                             const int col = nt * 8 + 2 * c + (e & 1);
                             const int pos = s.first_pos + (col0 + col) / p.per;
-                            const bool seen = here[gr] && col < cols && t <= pos &&
+                            const bool seen = (here >> gr & 1u) && col < cols && t <= pos &&
                                               (p.window == 0 || t > pos - p.window);
                             hidden |= (uint32_t)!seen << ((gr * NT + nt) * 4 + e);
                         }
             }
-            float y[kChunkGroups][NT][4];
+            float y[kChunkGroups][NT][4], sum[NT][2];
             bool high = false;
+            auto exps = [&](int nt) {
 #pragma unroll
-            for (int gr = 0; gr < kChunkGroups; ++gr)
+                for (int gr = 0; gr < kChunkGroups; ++gr)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                    for (int e = 0; e < 4; ++e)
+                        y[gr][nt][e] = fmaf(x[gr][nt][e], cs[nt][e & 1], -m[nt][e & 1]);
+                if (!full) {
+#pragma unroll
+                    for (int gr = 0; gr < kChunkGroups; ++gr)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (hidden & (1u << ((gr * NT + nt) * 4 + e))) y[gr][nt][e] = -INFINITY;
+                }
+                sum[nt][0] = sum[nt][1] = 0.0f;
+#pragma unroll
+                for (int gr = 0; gr < kChunkGroups; ++gr)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float v = fmaf(x[gr][nt][e], cs[nt][e & 1], -m[nt][e & 1]);
-                        if (hidden & (1u << ((gr * NT + nt) * 4 + e))) v = -INFINITY;
-                        y[gr][nt][e] = v;
-                        high |= v > kRaise;
+                        y[gr][nt][e] = ex2(y[gr][nt][e]);
+                        sum[nt][e & 1] += y[gr][nt][e];
                     }
+                high |= sum[nt][0] > kPMax || sum[nt][1] > kPMax;
+            };
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) exps(nt);
             if (__any_sync(0xFFFFFFFFu, high)) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         float top = kNoMax;
@@ -424,25 +456,20 @@ paged_attn_split_kernel(const PagedAttnParams p)
                             o[nt][j][k] *= f;
                             o[nt][j][k + 2] *= f;
                         }
-#pragma unroll
-                        for (int gr = 0; gr < kChunkGroups; ++gr)
-#pragma unroll
-                            for (int e = k; e < 4; e += 2)
-                                y[gr][nt][e] = hidden & (1u << ((gr * NT + nt) * 4 + e))
-                                                   ? -INFINITY
-                                                   : fmaf(x[gr][nt][e], cs[nt][k], -now);
                     }
+                    exps(nt);
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                l[nt][0] += sum[nt][0];
+                l[nt][1] += sum[nt][1];
             }
             uint32_t pf[kChunkGroups][NT][2];
 #pragma unroll
             for (int gr = 0; gr < kChunkGroups; ++gr)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        y[gr][nt][e] = ex2(y[gr][nt][e]);
-                        l[nt][e & 1] += y[gr][nt][e];
-                    }
                     pf[gr][nt][0] = transpose8x8(FP16::pack(y[gr][nt][0], y[gr][nt][1]));
                     pf[gr][nt][1] = transpose8x8(FP16::pack(y[gr][nt][2], y[gr][nt][3]));
                 }
@@ -450,14 +477,14 @@ paged_attn_split_kernel(const PagedAttnParams p)
             // ---- O^T += V^T P^T
 #pragma unroll
             for (int gr = 0; gr < kChunkGroups; ++gr) {
-                const uint8_t *base = stage + gr * kKVGroupBytes;
-                const uint2 v0 = lds8(base + vread), v1 = lds8(base + vread + 256);
-                const uint2 v2 = lds8(base + vread + 512), v3 = lds8(base + vread + 768);
-                uint32_t f01 = lds_u8(base + vsread) | (lds_u8(base + vsread + 32) << 8);
-                uint32_t f23 = lds_u8(base + vsread + 64) | (lds_u8(base + vsread + 96) << 8);
+                const uint32_t base = stage + gr * kKVGroupBytes;
+                const uint2 v0 = lds8_at<0>(base + vread), v1 = lds8_at<256>(base + vread);
+                const uint2 v2 = lds8_at<512>(base + vread), v3 = lds8_at<768>(base + vread);
+                uint32_t f01 = lds1_at<0>(base + vsread) | (lds1_at<32>(base + vsread) << 8);
+                uint32_t f23 = lds1_at<64>(base + vsread) | (lds1_at<96>(base + vsread) << 8);
                 if (!full) {  // bytes of keys that nobody sees may be anything
                     const int t = tok0 + gr * 16 + c;
-                    const int end = here[gr] ? blk_hi : 0;
+                    const int end = here >> gr & 1u ? blk_hi : 0;
                     if (t >= end) f01 &= 0xFF00u;
                     if (t + 4 >= end) f01 &= 0x00FFu;
                     if (t + 8 >= end) f23 &= 0xFF00u;
@@ -485,6 +512,8 @@ paged_attn_split_kernel(const PagedAttnParams p)
 #undef RQ_PV
                 }
             }
+            stage = stage == (kStages - 1) * kChunkBytes ? 0 : stage + kChunkBytes;
+            filled = filled == (kStages - 1) * kChunkBytes ? 0 : filled + kChunkBytes;
         }
 
         // ---- join the warps: O of column k in the warp's ring, 512 bytes each
@@ -501,7 +530,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
                 if (g == 0) stats[warp][col] = make_float2(m[nt][k], sum);
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<float2 *>(ring + col * 512 + (16 * g + 2 * j) * 4) =
+                    *reinterpret_cast<float2 *>(warp_o + col * 128 + 16 * g + 2 * j) =
                         make_float2(o[nt][j][k], o[nt][j][k + 2]);
             }
         __syncthreads();

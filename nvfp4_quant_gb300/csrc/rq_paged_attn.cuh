@@ -8,7 +8,8 @@
 namespace rq {
 
 constexpr float kNoMax = -3.0e38f;  // running maximum before any key is seen
-constexpr float kRaise = 8.0f;      // it is moved when a score exceeds it by more (in log2)
+constexpr float kPMax = 32768.0f;   // a sum of exponentials beyond it moves the maximum
+constexpr float kLeastScale = 1e-37f;  // of scores: -inf times it stays -inf
 
 __device__ __forceinline__ float ex2(float x)
 {

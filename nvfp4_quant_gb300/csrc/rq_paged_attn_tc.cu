@@ -39,7 +39,6 @@ constexpr int kThreads = 13 * 32;
 constexpr uint32_t kTileBytes = kTile * kD * 2;  // 32 KB
 // shared memory (from a 1024-byte boundary): Q0 Q1 K[2] V[2], then the small part
 constexpr uint32_t kQ = 0, kK = 2 * kTileBytes, kV = kK + 2 * kTileBytes, kSmall = kV + 2 * kTileBytes;
-constexpr float kPMax = 32768.0f;  // below fp16's largest value
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
 struct Small {
@@ -323,7 +322,7 @@ paged_attn_tc_kernel(const PagedAttnParams p)
             f = pw.x;
             back = pw.y;
         }
-        scale = p.scale * back / ld_f32(p.k_gs);
+        scale = fmaxf(p.scale * back / ld_f32(p.k_gs), kLeastScale);
 #pragma unroll 4
         for (int c = 0; c < 16; ++c) {
             uint4 v = make_uint4(0, 0, 0, 0);
