@@ -38,15 +38,25 @@ namespace rq {
 
 namespace {
 
-constexpr int kWarps = 8, kThreads = kWarps * 32;
+// Four warps a CTA, four CTAs an SM (registers): a CTA's warps meet at each
+// item's end, so fewer of them wait less (measured with 8, 4 and 2 warps:
+// 64 ragged sequences up to 4096 keys 48, 45 and 48 us, 32 sequences of 16
+// query columns 40, 34 and 35, one of 1000 keys 9.6, 9.1 and 9.6, 128 x 8192
+// keys 228, 228 and 237).
+constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kChunkGroups = 2, kChunk = kChunkGroups * 16;  // keys of one step of a warp
 constexpr int kStages = 3;
+// An item's overhead (queries, first copies, join) in chunks, for the cut into
+// shares (0, 4, 8, 16, 32: 56, 52, 46, 45, 49 us for the ragged sequences).
+constexpr int kStart = 16;
+constexpr int kBatch = 32 / kChunkGroups;  // chunks whose places a warp holds
+constexpr uint32_t kAll = (1u << kChunkGroups) - 1u;
 constexpr int kChunkBytes = kChunkGroups * kKVGroupBytes;
 constexpr int kSmem = kWarps * kStages * kChunkBytes;
 // Queries x heads of a KV head up to which a sequence is taken here and not by
 // the tensor-memory kernel.
 constexpr int kFewColumns = 32;
-constexpr int kMaxCtas = 512;      // grid limit (workspace slots)
+constexpr int kMaxCtas = 1024;     // grid limit (workspace slots)
 
 // A part: O [8 NT][128], m [8 NT], l [8 NT].
 template <int NT>
@@ -139,7 +149,20 @@ template <int NT>
 __device__ __forceinline__ int64_t seq_units(const PagedAttnParams &p, const Seq &s)
 {
     const Cut c = cut<NT>(p, s);
-    return (int64_t)p.hk * c.blocks * c.tiles;
+    return (int64_t)p.hk * c.blocks * (c.tiles + kStart);
+}
+
+// a / b for a >= 0: a 64-bit division is some 150 instructions, and a is
+// nearly always short.
+__device__ __forceinline__ int64_t div_small(int64_t a, int b)
+{
+    return a >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// Column of a sequence -> query and head of the group (one query: no division).
+__device__ __forceinline__ int query_of(const PagedAttnParams &p, const Seq &s, int col)
+{
+    return s.nq == 1 ? 0 : (int)((uint32_t)col / (uint32_t)p.per);
 }
 
 // Stores 8 NT columns' results: out (and lse) of column col from its sums.
@@ -147,7 +170,7 @@ template <typename DT, int VALS>
 __device__ __forceinline__ void store_out(const PagedAttnParams &p, const Seq &s, int head, int col,
                                           int d0, float (&v)[VALS], float m, float l)
 {
-    const int i = col / p.per, h = head * p.per + col % p.per;
+    const int i = query_of(p, s, col), h = head * p.per + col - i * p.per;
     const int64_t row = ((int64_t)(s.q0 + i) * p.hq + h);
     const float inv = out_factor(p, l);
     uint8_t *dst = static_cast<uint8_t *>(p.out) + (row * 128 + d0) * 2;
@@ -160,9 +183,10 @@ __device__ __forceinline__ void store_out(const PagedAttnParams &p, const Seq &s
 }
 
 template <typename DT, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, (NT == 1 ? 16 : 8) / kWarps)
 paged_attn_split_kernel(const PagedAttnParams p)
 {
+    static_assert(kStages * kChunkBytes >= 8 * NT * 128 * 4, "a warp's ring holds its part of O at the end");
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int64_t scan[kWarps];
     __shared__ int start_seq;
@@ -177,7 +201,8 @@ paged_attn_split_kernel(const PagedAttnParams p)
                    (int64_t)blockIdx.x * 2 * kPartFloats<NT>;
 
     // ---- this CTA's share: units (head, block, chunk of keys) of all
-    // sequences in order, cut into equal runs.  Thread t adds up the units of
+    // sequences in order, each item (head, block) begun by kStart units that
+    // stand for its overhead, cut into equal runs.  Thread t adds up the units of
     // its run of sequences; the thread whose run holds the first unit finds it.
     const int per_thread = (p.n_seqs + kThreads - 1) / kThreads;
     const int b0 = min(p.n_seqs, (int)threadIdx.x * per_thread), b1 = min(p.n_seqs, b0 + per_thread);
@@ -197,10 +222,10 @@ paged_attn_split_kernel(const PagedAttnParams p)
         total += scan[w];
     }
     // at least a chunk per warp, where there is enough
-    const int64_t n = max((int64_t)1, min((int64_t)gridDim.x, total / kWarps));
-    const int64_t i0 = blockIdx.x;
-    int64_t u = i0 < n ? total * i0 / n : total;
-    const int64_t u_end = i0 < n ? total * (i0 + 1) / n : total;
+    const int n = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kWarps));
+    const int64_t i0 = blockIdx.x, each = div_small(total, n), more = total - each * n;
+    int64_t u = i0 < n ? each * i0 + min(i0, more) : total;
+    const int64_t u_end = i0 < n ? u + each + (i0 < more) : total;
     if (upto - mine <= u && u < upto) {
         int64_t rem = u - (upto - mine);
         int b = b0;
@@ -234,20 +259,25 @@ paged_attn_split_kernel(const PagedAttnParams p)
     Seq s = load_seq(p, b);
     Cut ct = cut<NT>(p, s);
     while (u < u_end) {
-        const int64_t all = (int64_t)p.hk * ct.blocks * ct.tiles;
+        const int cost = ct.tiles + kStart;
+        const int64_t all = (int64_t)p.hk * ct.blocks * cost;
         if (rem >= all) {
             rem -= all;
             s = load_seq(p, ++b);
             ct = cut<NT>(p, s);
             continue;
         }
-        const int item = (int)(rem / ct.tiles), tile0 = (int)(rem - (int64_t)item * ct.tiles);
+        const int item = (int)div_small(rem, cost), from = (int)(rem - (int64_t)item * cost);
+        const int take = (int)min((int64_t)(cost - from), u_end - u);
+        u += take;
+        rem += take;
+        const int tile0 = max(0, from - kStart), ntile = from + take - kStart - tile0;
+        if (ntile <= 0) continue;  // no more than the item's overhead
         const int head = item / ct.blocks, block = item - head * ct.blocks;
-        const int ntile = (int)min((int64_t)(ct.tiles - tile0), u_end - u);
         const int col0 = block * 8 * NT, cols = min(8 * NT, s.nq * p.per - col0);
         // keys that the block's columns see: all of [need_lo, need_hi) by every
         // one, nothing from blk_hi on by any
-        const int i_first = col0 / p.per, i_last = (col0 + cols - 1) / p.per;
+        const int i_first = query_of(p, s, col0), i_last = query_of(p, s, col0 + cols - 1);
         const int blk_hi = s.first_pos + i_last + 1;
         const int need_hi = s.first_pos + i_first + 1;
         const int need_lo = p.window > 0 ? blk_hi - p.window : 0;
@@ -257,10 +287,11 @@ paged_attn_split_kernel(const PagedAttnParams p)
                                ? (t1 - t0 - warp * kChunk + kWarps * kChunk - 1) / (kWarps * kChunk)
                                : 0;  // of this warp
 
-        // ---- groups of the warp's chunks, 16 chunks at a time: lane 2 i + j
-        // holds where group j of chunk i lies in the cache (-1: nowhere)
+        // ---- groups of the warp's chunks, 32 groups at a time: lane kChunkGroups
+        // i + j holds where group j of chunk i lies in the cache (-1: nowhere)
         auto find = [&](int batch) {
-            const int token = t0 + (warp + kWarps * (batch * 16 + (lane >> 1))) * kChunk + (lane & 1) * 16;
+            const int token = t0 + (warp + kWarps * (batch * kBatch + lane / kChunkGroups)) * kChunk +
+                              lane % kChunkGroups * 16;
             int at = -1;
             if (token < t1) {
                 const int slot = token >> 4, page = slot / p.groups;
@@ -273,7 +304,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
         auto fetch = [&](int i, int from, uint32_t stage) {  // starts the copies of chunk i
 #pragma unroll
             for (int gr = 0; gr < kChunkGroups; ++gr) {
-                const int at = __shfl_sync(0xFFFFFFFFu, from, (i & 15) * 2 + gr);
+                const int at = __shfl_sync(0xFFFFFFFFu, from, i % kBatch * kChunkGroups + gr);
                 if (at >= 0 && i < chunks) {
                     const uint8_t *src = p.pool + (int64_t)at * kKVGroupBytes + lane * 16;
                     const uint32_t d = stage + gr * kKVGroupBytes;
@@ -300,7 +331,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
             const int col = nt * 8 + g;
             uint4 v[4] = {};
             if (col < cols) {
-                const int i = (col0 + col) / p.per, h = head * p.per + (col0 + col) % p.per;
+                const int i = query_of(p, s, col0 + col), h = head * p.per + col0 + col - i * p.per;
                 const uint8_t *src = static_cast<const uint8_t *>(p.q) +
                                      ((s.q0 + i) * p.q_stride + (int64_t)h * 128 + 32 * c) * 2;
 #pragma unroll
@@ -324,10 +355,17 @@ paged_attn_split_kernel(const PagedAttnParams p)
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                float e[8];
-                unpack8<DT>(v[k], e);
+                if (std::is_same<DT, BF16>::value) {
+                    float e[8];
+                    unpack8<DT>(v[k], e);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) qf[nt][4 * k + j] = FP16::pack(e[2 * j] * f, e[2 * j + 1] * f);
+                    for (int j = 0; j < 8; ++j) e[j] *= f;
+                    v[k] = pack8<FP16>(e);
+                }
+                qf[nt][4 * k] = v[k].x;
+                qf[nt][4 * k + 1] = v[k].y;
+                qf[nt][4 * k + 2] = v[k].z;
+                qf[nt][4 * k + 3] = v[k].w;
             }
             const float scale = fmaxf(p.scale * inv_kgs * back, kLeastScale);
             cs[nt][0] = __shfl_sync(0xFFFFFFFFu, scale, 8 * c);
@@ -346,15 +384,15 @@ paged_attn_split_kernel(const PagedAttnParams p)
         for (int it = 0; it < chunks; ++it) {
             cp_async_wait<kStages - 2>();
             __syncwarp();  // everyone's copies have landed; everyone is done with the stage before
-            if (it > 0 && (it & 15) == 0) {
+            if (it > 0 && it % kBatch == 0) {
                 near = far;
-                far = find((it >> 4) + 1);
+                far = find(it / kBatch + 1);
                 near_ok = __ballot_sync(0xFFFFFFFFu, near >= 0);
             }
-            fetch(it + kStages - 1, (it & 15) + kStages - 1 < 16 ? near : far, filled);
+            fetch(it + kStages - 1, it % kBatch + kStages - 1 < kBatch ? near : far, filled);
             const int tok0 = t0 + (warp + kWarps * it) * kChunk;
-            const uint32_t here = near_ok >> ((it & 15) * 2);  // bit gr: the group is readable
-            const bool full = tok0 >= need_lo && tok0 + kChunk <= need_hi && (here & 3u) == 3u;
+            const uint32_t here = near_ok >> (it % kBatch * kChunkGroups);  // bit gr: the group is readable
+            const bool full = tok0 >= need_lo && tok0 + kChunk <= need_hi && (here & kAll) == kAll;
 
             // ---- S^T = K Q^T
             float x[kChunkGroups][NT][4];
@@ -400,7 +438,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
                         for (int e = 0; e < 4; ++e) {
                             const int t = tok0 + gr * 16 + tok_of_row(g) + (e >> 1) * 8;
                             const int col = nt * 8 + 2 * c + (e & 1);
-                            const int pos = s.first_pos + (col0 + col) / p.per;
+                            const int pos = s.first_pos + query_of(p, s, col0 + col);
                             const bool seen = (here >> gr & 1u) && col < cols && t <= pos &&
                                               (p.window == 0 || t > pos - p.window);
                             hidden |= (uint32_t)!seen << ((gr * NT + nt) * 4 + e);
@@ -564,8 +602,6 @@ paged_attn_split_kernel(const PagedAttnParams p)
         if (threadIdx.x == 0 && ntile != ct.tiles)
             info[tile0 == 0] = PartInfo{1, tile0 + ntile == ct.tiles, b, head, block};
         __syncthreads();
-        u += ntile;
-        rem += ntile;
     }
 }
 
