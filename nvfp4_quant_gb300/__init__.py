@@ -10,6 +10,7 @@ runs in the CUDA kernels of librq.so; there is no other code path.  If the
 library has not been built, importing works but the first call raises.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -435,54 +436,64 @@ def rq_qk_rmsnorm_rope_fp8_dynamic(q, k, q_weight, k_weight, eps, positions, cos
 
 
 # ------------------------------------------------------- paged NVFP4 KV cache
-def _same_device(ref, *others):
+# These calls are short (a decode step's append runs for 4 us on the GPU), so
+# their checks are kept to the cheapest torch queries.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _same_device(*tensors):
     """The index of the device that every given tensor lies on."""
-    if not ref.is_cuda:
-        raise ValueError("every tensor argument must be a CUDA tensor (got one on %s)" % ref.device)
-    dev = ref.device
-    for t in others:
-        if t is not None and t.device != dev:
-            raise ValueError("every tensor argument must lie on %s (got one on %s)" % (dev, t.device))
-    return dev.index
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev or dev < 0:
+            bad = tensors[0] if dev < 0 else t
+            raise ValueError("every tensor argument must be a CUDA tensor on one device (got %s and %s)"
+                             % (tensors[0].device, bad.device))
+    return dev
 
 
 def _call_on(dev, fn, args, stream):
     """fn(*args, stream) with the tensors' device current; stream None is that
     device's current stream."""
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    stream = getattr(stream, "cuda_stream", stream)
+        stream = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
+    else:
+        stream = getattr(stream, "cuda_stream", stream)
     if torch.cuda.current_device() == dev:
-        _check(fn(*args, stream))
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, stream))
+            status = fn(*args, stream)
+    if status:
+        _check(status)
 
 
 def _typed(t, dtype, numel, name):
     """A contiguous tensor of at least numel elements of a type."""
-    if t is None or t.dtype != dtype or not t.is_contiguous() or t.numel() < numel:
+    if t is None or t.dtype != dtype or t.numel() < numel or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of at least %d elements"
                          % (name, str(dtype).replace("torch.", ""), numel))
     return t.data_ptr()
 
 
 def _cache(kv_pool, page_size, heads):
-    if kv_pool.dtype != torch.uint8 or kv_pool.dim() != 3 or not kv_pool.is_contiguous() or \
-            kv_pool.shape[1] != heads or kv_pool.shape[2] != page_size * 144:
+    shape = kv_pool.shape
+    if len(shape) != 3 or kv_pool.dtype != torch.uint8 or shape[1] != heads or \
+            shape[2] != page_size * 144 or not kv_pool.is_contiguous():
         raise ValueError("kv_pool must be a contiguous uint8 [num_pages, n_kv_heads, page_size * 144] "
                          "tensor with %d heads" % heads)
-    return kv_pool.data_ptr(), kv_pool.shape[0], int(page_size)
+    return kv_pool.data_ptr(), shape[0], int(page_size)
 
 
 def _head_rows(t, name, like=None):
-    if t.dim() != 3 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or stride[2] != 1 or stride[1] != shape[2]:
         raise ValueError("%s must be a [tokens, heads, head_dim] view with contiguous heads" % name)
-    if like is not None and (t.shape[0] != like.shape[0] or t.dtype != like.dtype
-                             or t.shape[2] != like.shape[2]):
+    if like is not None and (shape[0] != like.shape[0] or t.dtype != like.dtype
+                             or shape[2] != like.shape[2]):
         raise ValueError("%s must match q in token count, head_dim and dtype" % name)
     # a single token's stride says nothing (torch leaves any value there)
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return t.data_ptr(), stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
 
 def rq_qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos_sin_cache,
@@ -577,6 +588,7 @@ def rq_paged_extend_attn_nvfp4(q, kv_pool, page_size, block_table, q_starts, kv_
                 v_global_scale, sm_scale, out, workspace, window, lse, stream)
 
 
+@functools.lru_cache(maxsize=None)
 def rq_paged_attn_nvfp4_workspace_bytes(n_q_heads, n_kv_heads):
     return int(lib().rq_paged_attn_nvfp4_workspace_bytes(n_q_heads, n_kv_heads))
 
@@ -659,26 +671,12 @@ def add_rmsnorm_fp8(x, residual, weight, eps, scale, with_norm_out=False, in_pla
     return res_out, q, y
 
 
-class _on_stream:
-    """Allocations inside come from `stream`'s pool, so that a buffer's memory
-    is not handed out again while that stream still uses it.  None: the current
-    stream of the device, nothing to do."""
-
-    def __init__(self, stream, device):
-        if stream is None:
-            self.guard = None
-        else:
-            if not isinstance(stream, torch.cuda.Stream):
-                stream = torch.cuda.ExternalStream(stream, device=device)
-            self.guard = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *e):
-        if self.guard is not None:
-            self.guard.__exit__(*e)
+def _on_stream(stream, device):
+    """A context in which allocations come from `stream`'s pool, so that a
+    buffer's memory is not handed out again while that stream still uses it."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
 
 
 def nvfp4_kv_pool(num_pages, n_kv_heads, page_size, device="cuda"):
@@ -693,8 +691,11 @@ def qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos_si
                              k_global_scale, v_global_scale, kv_pool, slots, page_size, stream=None):
     """Allocate q_out (torch) and run rq_qkv_rope_nvfp4_kv_append.  Returns
     q_out [T, Hq, 128]."""
-    with _on_stream(stream, q.device):
+    if stream is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    else:
+        with _on_stream(stream, q.device):
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     rq_qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos_sin_cache,
                                 k_global_scale, v_global_scale, q_out, kv_pool, slots, page_size,
                                 stream)
@@ -702,12 +703,14 @@ def qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos_si
 
 
 def _attn_buffers(q, kv_pool, with_lse, workspace, stream):
-    with _on_stream(stream, q.device):
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if with_lse else None
-        if workspace is None:
-            workspace = torch.empty((rq_paged_attn_nvfp4_workspace_bytes(q.shape[1], kv_pool.shape[1]),),
-                                    dtype=torch.uint8, device=q.device)
+    if stream is not None:
+        with _on_stream(stream, q.device):
+            return _attn_buffers(q, kv_pool, with_lse, workspace, None)
+    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if with_lse else None
+    if workspace is None:
+        workspace = torch.empty((rq_paged_attn_nvfp4_workspace_bytes(q.shape[1], kv_pool.shape[1]),),
+                                dtype=torch.uint8, device=q.device)
     return out, lse, workspace
 
 
