@@ -59,8 +59,7 @@ __device__ __forceinline__ float rcp_approx(float x)
 // arithmetic (fp32 pairs, about 2^-44 of M; products of inputs exact), and
 // each open code decided by comparing y gs with border * sf, both sides exact
 // where the inputs make a tie possible.  (fp64 would do the same, but this
-// GPU's few fp64 lanes took 10 us a step: 4096 tokens of 16 + 8 heads 213 us
-// against 15.)
+// GPU's few fp64 lanes took 10 us a step: 4096 tokens of 16 + 8 heads 213 us.)
 __device__ __forceinline__ F2 f2_mul(const F2 &a, const F2 &b)
 {
     F2 p = two_prod(a.h, b.h);
@@ -140,14 +139,30 @@ __device__ __forceinline__ uint32_t block_codes_exact(const F2 (&y)[8], uint32_t
     return c;
 }
 
-// The step's codes, decided as above: {codes of elements 8 l .., codes of 64 +
-// 8 l .., scale byte of the lower block, of the upper block}.  Every lane of
-// the warp calls it.
+// The codes of K row `head` of token tok, decided as above: {codes of elements
+// 8 l .., codes of 64 + 8 l .., scale byte of the lower block, of the upper
+// block}.  Every lane of the warp calls it (head past the last: any codes).  It
+// reads the row again rather than take it, which keeps the common path's
+// registers few.
 template <typename DT>
-__device__ __noinline__ uint4 key_codes_exact(uint4 xl, uint4 xh, uint4 wl, uint4 wh, bool normed,
-                                              const float *cs, float eps, float gs)
+__device__ __noinline__ uint4 key_codes_exact(const KVAppendParams &p, int64_t tok, int head, float gs)
 {
     const int l = threadIdx.x & 7;
+    uint4 xl = make_uint4(0, 0, 0, 0), xh = xl, wl = xl, wh = xl;
+    if (head < p.hk) {
+        const uint8_t *src = static_cast<const uint8_t *>(p.k) + (tok * p.k_stride + (int64_t)head * kD) * 2;
+        xl = ld_stream16(src + l * 16);
+        xh = ld_stream16(src + 128 + l * 16);
+    }
+    const bool normed = p.kw != nullptr;
+    if (normed) {
+        wl = ld_keep16(static_cast<const uint8_t *>(p.kw) + l * 16);
+        wh = ld_keep16(static_cast<const uint8_t *>(p.kw) + 128 + l * 16);
+    }
+    int pos = ld_s32(p.pos + tok);
+    pos = pos < 0 ? 0 : (pos >= p.max_pos ? (int)(p.max_pos - 1) : pos);
+    const float *cs = p.cos_sin + (int64_t)pos * kD;
+    const float eps = p.eps;
     float x0[8], x1[8];
     unpack8<DT>(xl, x0);
     unpack8<DT>(xh, x1);
@@ -306,8 +321,8 @@ __device__ __forceinline__ void load_pairs(const float *src, float2 (&f)[4])
 }
 
 template <typename DT, int STEPS>
-__global__ void __launch_bounds__(kAppendBlock, 4)
-kv_append_kernel(const KVAppendParams p)
+__global__ void __launch_bounds__(kAppendBlock, 5)
+kv_append_kernel(const __grid_constant__ KVAppendParams p)
 {
     pdl_trigger();
     pdl_wait();
@@ -323,8 +338,13 @@ kv_append_kernel(const KVAppendParams p)
     const int step_g = (int)(nwarps - step_tok * units);
     int64_t tok = warp0 / units;
     int g = (int)(warp0 - tok * units);
+    // Where the warps are a multiple of the units, a warp would meet the same
+    // unit of every token, and those of K take longer than those of Q: its unit
+    // then moves on by one a turn (all units of a token are in one turn).
+    int turn = 0;
     while (tok < p.n_tokens) {
-        const int s0 = g * STEPS;
+        const int unit = g + turn < units ? g + turn : g + turn - units;
+        const int s0 = unit * STEPS;
         uint4 xl[STEPS], xh[STEPS];
 #pragma unroll
         for (int u = 0; u < STEPS; ++u) {
@@ -423,7 +443,7 @@ kv_append_kernel(const KVAppendParams p)
                 c0 = key_codes(a, m0 * rstd, k_gs, f0, unsure);
                 c1 = key_codes(b, m1 * rstd, k_gs, f1, unsure);
                 if (__any_sync(0xFFFFFFFFu, unsure)) {
-                    const uint4 r = key_codes_exact<DT>(xl[u], xh[u], wl, wh, wp != nullptr, cs, p.eps, k_gs);
+                    const uint4 r = key_codes_exact<DT>(p, tok, h, k_gs);
                     c0 = r.x;
                     c1 = r.y;
                     f0 = r.z;
@@ -447,6 +467,7 @@ kv_append_kernel(const KVAppendParams p)
                 }
             }
         }
+        if (step_g == 0 && ++turn == units) turn = 0;
         tok += step_tok;
         g += step_g;
         if (g >= units) {
@@ -486,9 +507,10 @@ cudaError_t launch_kv_append(const KVAppendParams &p, cudaStream_t stream)
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     // Few steps: one a warp, so that they spread over the SMs.  Otherwise two
-    // a unit at 16 warps an SM (measured, 4096 tokens of 16 + 8 heads and
-    // 32,749 of 32 + 8: 20.6 and 145 us; one step a unit 22.4 and 205, four
-    // 23.2 and 151, two at 20 warps, with spills, 20.9 and 149).
+    // a unit at 20 warps an SM (measured, 4096 tokens of 16 + 8 heads and
+    // 32,749 of 32 + 8: 19.8 and 142 us; at 16 warps 20.1 and 147, at 24, with
+    // more spills, 20.5 and 142; one step a unit 20.4 and 170, four 22.5 and
+    // 149).
     return p.n_tokens * steps_of(p) < (int64_t)device_sms(dev) * 32
                ? launch_steps<DT, 1>(p, dev, stream)
                : launch_steps<DT, 2>(p, dev, stream);
