@@ -80,10 +80,10 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
                  :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add) : "memory");
 }
-__device__ __forceinline__ void mma_commit(uint64_t *bar)
+__device__ __forceinline__ void mma_commit(uint32_t bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 :: "r"(smem_addr(bar)) : "memory");
+                 :: "r"(bar) : "memory");
 }
 __device__ __forceinline__ void tm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -139,9 +139,9 @@ __device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count)
 {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(smem_addr(bar)), "r"(count) : "memory");
 }
-__device__ __forceinline__ void bar_arrive(uint64_t *bar)
+__device__ __forceinline__ void bar_arrive(uint32_t bar)
 {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_addr(bar)) : "memory");
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(bar) : "memory");
 }
 __device__ __forceinline__ unsigned long long now_ns()
 {
@@ -151,13 +151,13 @@ __device__ __forceinline__ unsigned long long now_ns()
 }
 // Waits until the barrier's phase of the given parity is over; gives up after
 // kWaitNs, or when another role of the CTA has (false).
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile int *failed)
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *failed)
 {
     unsigned long long start = 0;
     for (uint32_t n = 0;; ++n) {
         uint32_t done;
         asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
-                     : "=r"(done) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+                     : "=r"(done) : "r"(bar), "r"(parity) : "memory");
         if (done) return true;
         if ((n & 63) == 63) {
             if (*failed) return false;
@@ -179,7 +179,7 @@ __device__ __forceinline__ bool elect_one()
 }
 
 // The same for a whole warp: every lane gets one answer.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *failed)
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *failed)
 {
     return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, failed));
 }
@@ -210,21 +210,54 @@ __device__ __forceinline__ void load_row(Row &r, const uint8_t *codes, const uin
     asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(r.f.x), "=r"(r.f.y) : "l"(scales));
 }
 
-__device__ __forceinline__ void decode_row(const Row &r, uint8_t *tile, int row)
+// Decodes into the row at shared address `to` (swizzled: `to` holds (row & 7)
+// << 4 in the bits that the chunk's number is xored into), 32 channels at a time
+// in the order that keeps uses away from what they wait for.
+__device__ __forceinline__ void decode_row(const Row &r, uint32_t to)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t w[4] = {r.c[i].x, r.c[i].y, r.c[i].z, r.c[i].w};
         const uint32_t two = e4m3_pair(((i & 2) ? r.f.y : r.f.x) >> ((i & 1) * 16));
+        const uint32_t f[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
+        uint32_t x[16];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint32_t f = __byte_perm(two, two, j < 2 ? 0x1010 : 0x3232);
-            sts16(tile + tile_at(row, 4 * i + j),
-                  make_uint4(FP16::mul2(e2m1_pair<0>(w[j]), f), FP16::mul2(e2m1_pair<1>(w[j]), f),
-                             FP16::mul2(e2m1_pair<2>(w[j]), f), FP16::mul2(e2m1_pair<3>(w[j]), f)));
+        for (int c = 0; c < 4; ++c) {
+            x[4 * c] = e2m1_pair<0>(w[c]);
+            x[4 * c + 1] = e2m1_pair<1>(w[c]);
+            x[4 * c + 2] = e2m1_pair<2>(w[c]);
+            x[4 * c + 3] = e2m1_pair<3>(w[c]);
         }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = FP16::mul2(x[k], f[k >> 3]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                         :: "r"((to ^ ((4 * (i & 1) + c) << 4)) + (i >> 1) * (kTileBytes / 2)), "r"(x[4 * c]),
+                            "r"(x[4 * c + 1]), "r"(x[4 * c + 2]), "r"(x[4 * c + 3]) : "memory");
     }
 }
+
+// Where a token lies: its page's place in the sequence's table and its group in
+// the page, from tile to tile without a division.
+struct Place {
+    int at, page, in;
+    __device__ __forceinline__ Place(int token, int groups) : at(token)
+    {
+        page = (token >> 4) / groups;
+        in = (token >> 4) - page * groups;
+    }
+    __device__ __forceinline__ void next(int groups, int pages, int rest)  // a tile: 8 groups
+    {
+        at += kTile;
+        page += pages;
+        in += rest;
+        if (in >= groups) {
+            in -= groups;
+            ++page;
+        }
+    }
+};
 
 template <typename DT>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -342,6 +375,10 @@ paged_attn_tc_kernel(const PagedAttnParams p)
     __syncthreads();
     tm_fence_after();
     const uint32_t tmem = sm.tmem;
+    struct {
+        uint32_t k_full, k_empty, v_full, v_empty, s_full, p_full, pv_done, drained;
+    } const bars = {smem_addr(sm.k_full), smem_addr(sm.k_empty), smem_addr(sm.v_full),  smem_addr(sm.v_empty),
+                    smem_addr(sm.s_full), smem_addr(sm.p_full),  smem_addr(sm.pv_done), smem_addr(&sm.drained)};
     volatile int *failed = &sm.failed;
 
     if (warp == 12) {
@@ -362,31 +399,31 @@ paged_attn_tc_kernel(const PagedAttnParams p)
                     const uint32_t off = ((k >> 2) * (kTileBytes / 2) + (k & 3) * 32) >> 4;
                     mma_ss(tmem + kColS + tt * 128, a + off, bk + off, kIdescQK, k > 0);
                 }
-                mma_commit(&sm.s_full[tt]);
-                if (tt == 1) mma_commit(&sm.k_empty[j & 1]);
+                mma_commit(bars.s_full + 8 * (tt));
+                if (tt == 1) mma_commit(bars.k_empty + 8 * (j & 1));
             }
         };
-        bool ok = n > 0 && warp_wait(&sm.k_full[0], 0, failed);
+        bool ok = n > 0 && warp_wait(bars.k_full + 8 * (0), 0, failed);
         if (ok) {
             tm_fence_after();
             qk(0, 0);
             qk(1, 0);
         }
         for (int j = 0; ok && j < n; ++j) {
-            ok = warp_wait(&sm.v_full[j & 1], (j >> 1) & 1, failed) &&
-                 (j + 1 == n || warp_wait(&sm.k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, failed));
+            ok = warp_wait(bars.v_full + 8 * (j & 1), (j >> 1) & 1, failed) &&
+                 (j + 1 == n || warp_wait(bars.k_full + 8 * ((j + 1) & 1), ((j + 1) >> 1) & 1, failed));
             const uint64_t bv = dv + (j & 1) * (kTileBytes >> 4);
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
-                if (!ok || !(ok = warp_wait(&sm.p_full[tt], j & 1, failed))) break;
+                if (!ok || !(ok = warp_wait(bars.p_full + 8 * (tt), j & 1, failed))) break;
                 tm_fence_after();
                 if (lead) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         mma_ts(tmem + kColO + tt * 128, tmem + kColS + tt * 128 + k * 8, bv + k * (2048 >> 4),
                                kIdescPV, j > 0 || k > 0);
-                    mma_commit(&sm.pv_done[tt]);
-                    if (tt == 1) mma_commit(&sm.v_empty[j & 1]);
+                    mma_commit(bars.pv_done + 8 * (tt));
+                    if (tt == 1) mma_commit(bars.v_empty + 8 * (j & 1));
                 }
                 if (j + 1 < n) qk(tt, j + 1);
             }
@@ -394,50 +431,55 @@ paged_attn_tc_kernel(const PagedAttnParams p)
         // no product may outlive the operands and the tensor memory, also
         // when the loop gave up
         int none = 0;
-        if (lead) mma_commit(&sm.drained);
-        warp_wait(&sm.drained, 0, &none);
+        if (lead) mma_commit(bars.drained);
+        warp_wait(bars.drained, 0, &none);
     } else if (warp >= 8) {
         // ---------------------------------------------------------- keys and values
         const int tok = threadIdx.x - 8 * 32;  // of the tile
-        auto find = [&](int j) -> const uint8_t * {  // the token's group
-            const int at = lo + j * kTile + tok;
-            if (j >= n || at >= hi) return nullptr;
-            const int slot = at >> 4, page = slot / p.groups;
-            const int id = ld_s32(p.table + (int64_t)b * p.table_stride + page);
-            if (id < 0 || id >= p.num_pages) return nullptr;
-            return p.pool + (((int64_t)id * p.hk + head) * p.groups + (slot - page * p.groups)) * kKVGroupBytes;
+        const int32_t *table = p.table + (int64_t)b * p.table_stride;
+        const int pages = 8 / p.groups, rest = 8 - pages * p.groups, in_group = tok & 15;  // lo: a multiple of 16
+        const uint8_t *k_pool = p.pool + (int64_t)head * p.groups * kKVGroupBytes + in_group * 64;
+        const int64_t page_bytes = (int64_t)p.hk * p.groups * kKVGroupBytes;
+        Place place(lo + tok, p.groups);
+        // page ids a tile further ahead than the codes (-1: no such token)
+        int in = place.in, id = place.at < hi ? ld_s32(table + place.page) : -1;
+        auto step = [&]() -> const uint8_t * {  // the next tile's row
+            const uint8_t *at = id < 0 || id >= p.num_pages ? nullptr : k_pool + id * page_bytes + in * kKVGroupBytes;
+            place.next(p.groups, pages, rest);
+            in = place.in;
+            id = place.at < hi ? ld_s32(table + place.page) : -1;
+            return at;
         };
-        const int in_group = tok & 15;  // lo is a multiple of 16
-        auto load_k = [&](Row &x, const uint8_t *g) {
+        auto load_k = [&](Row &x, const uint8_t *at) {
             x = Row{};
-            if (g != nullptr) load_row(x, g + kKVCodesK + in_group * 64, g + kKVScalesK + in_group * 8);
+            if (at != nullptr) load_row(x, at + kKVCodesK, at + kKVScalesK - in_group * 56);
         };
-        auto load_v = [&](Row &x, const uint8_t *g) {
+        auto load_v = [&](Row &x, const uint8_t *at) {
             x = Row{};
-            if (g != nullptr) load_row(x, g + kKVCodesV + in_group * 64, g + kKVScalesV + in_group * 8);
+            if (at != nullptr) load_row(x, at + kKVCodesV, at + kKVScalesV - in_group * 56);
         };
+        const uint32_t to = smem_addr(smem) + tok * 128 + ((tok & 7) << 4);
         Row k, v;
-        const uint8_t *g = find(0), *g_next = find(1);
+        const uint8_t *g = step();
         load_k(k, g);
         load_v(v, g);
         for (int j = 0; j < n; ++j) {
             const int st = j & 1;
-            if (j >= 2 && !warp_wait(&sm.k_empty[st], ((j >> 1) + 1) & 1, failed)) break;
+            if (j >= 2 && !warp_wait(bars.k_empty + 8 * st, ((j >> 1) + 1) & 1, failed)) break;
             const uint32_t seen = __ballot_sync(0xFFFFFFFFu, g != nullptr);
             if (lane == 0) sm.seen[j & 3][warp - 8] = seen;
-            decode_row(k, smem + kK + st * kTileBytes, tok);
+            decode_row(k, to + kK + st * kTileBytes);
             async_proxy_fence();
             __syncwarp();
-            if (lane == 0) bar_arrive(&sm.k_full[st]);
-            load_k(k, g_next);
-            if (j >= 2 && !warp_wait(&sm.v_empty[st], ((j >> 1) + 1) & 1, failed)) break;
-            decode_row(v, smem + kV + st * kTileBytes, tok);
+            if (lane == 0) bar_arrive(bars.k_full + 8 * st);
+            g = step();
+            load_k(k, g);
+            if (j >= 2 && !warp_wait(bars.v_empty + 8 * st, ((j >> 1) + 1) & 1, failed)) break;
+            decode_row(v, to + kV + st * kTileBytes);
             async_proxy_fence();
             __syncwarp();
-            if (lane == 0) bar_arrive(&sm.v_full[st]);
-            load_v(v, g_next);
-            g = g_next;
-            g_next = find(j + 2);
+            if (lane == 0) bar_arrive(bars.v_full + 8 * st);
+            load_v(v, g);
         }
     } else {
         // ---------------------------------------------------------- softmax
@@ -448,7 +490,7 @@ paged_attn_tc_kernel(const PagedAttnParams p)
         const int row_lo = p.window > 0 ? row_hi - p.window : 0;
         float m = kNoMax, l = 0.0f;
         for (int j = 0; j < n; ++j) {
-            if (!warp_wait(&sm.s_full[t], j & 1, failed)) break;
+            if (!warp_wait(bars.s_full + 8 * (t), j & 1, failed)) break;
             tm_fence_after();
             auto visible = [&](int c) {  // of the tile's columns 32 c ..
                 const int first = lo + j * kTile + 32 * c, below = row_hi - first, from = row_lo - first;
@@ -521,7 +563,7 @@ paged_attn_tc_kernel(const PagedAttnParams p)
                 m = top;
                 l *= f;
                 if (j > 0) {
-                    if (!warp_wait(&sm.pv_done[t], (j - 1) & 1, failed)) break;
+                    if (!warp_wait(bars.pv_done + 8 * (t), (j - 1) & 1, failed)) break;
                     tm_fence_after();
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
@@ -542,11 +584,11 @@ paged_attn_tc_kernel(const PagedAttnParams p)
             tm_wait_st();
             tm_fence_before();
             __syncwarp();
-            if (lane == 0) bar_arrive(&sm.p_full[t]);
+            if (lane == 0) bar_arrive(bars.p_full + 8 * (t));
         }
         // ---------------------------------------------------------- last step
         if (n > 0) {
-            warp_wait(&sm.pv_done[t], (n - 1) & 1, failed);
+            warp_wait(bars.pv_done + 8 * (t), (n - 1) & 1, failed);
             tm_fence_after();
         }
         const float inv = *failed ? __uint_as_float(0x7FC00000u) : out_factor(p, l);
