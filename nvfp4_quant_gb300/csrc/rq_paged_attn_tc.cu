@@ -238,24 +238,50 @@ __device__ __forceinline__ void decode_row(const Row &r, uint32_t to)
     }
 }
 
-// Where a token lies: its page's place in the sequence's table and its group in
-// the page, from tile to tile without a division.
-struct Place {
-    int at, page, in;
-    __device__ __forceinline__ Place(int token, int groups) : at(token)
+// A producer thread's token of each tile: where it lies, from tile to tile
+// without a division, and the page id of one tile further ahead.
+struct Feed {
+    int tok, hi, at, page, in, pages, rest, id;
+    const int32_t *table;
+    const uint8_t *pool;
+    int64_t page_bytes;
+
+    __device__ __forceinline__ int page_id() const { return at < hi ? ld_s32(table + page) : -1; }
+
+    __device__ __forceinline__ void start(const PagedAttnParams &p, int seq, int head, int lo, int hi_, int tok_)
     {
-        page = (token >> 4) / groups;
-        in = (token >> 4) - page * groups;
+        tok = tok_;
+        hi = hi_;
+        at = lo + tok;
+        page = (at >> 4) / p.groups;
+        in = (at >> 4) - page * p.groups;
+        pages = 8 / p.groups;  // a tile is 8 groups
+        rest = 8 - pages * p.groups;
+        table = p.table + (int64_t)seq * p.table_stride;
+        pool = p.pool + (int64_t)head * p.groups * kKVGroupBytes;
+        page_bytes = (int64_t)p.hk * p.groups * kKVGroupBytes;
+        id = page_id();
     }
-    __device__ __forceinline__ void next(int groups, int pages, int rest)  // a tile: 8 groups
+
+    // The group of the tile's token (null: none that can be read); on to the next tile.
+    __device__ __forceinline__ const uint8_t *step(const PagedAttnParams &p)
     {
+        const uint8_t *g = id < 0 || id >= p.num_pages ? nullptr : pool + id * page_bytes + in * kKVGroupBytes;
         at += kTile;
         page += pages;
         in += rest;
-        if (in >= groups) {
-            in -= groups;
+        if (in >= p.groups) {
+            in -= p.groups;
             ++page;
         }
+        id = page_id();
+        return g;
+    }
+
+    __device__ __forceinline__ void load(Row &r, const uint8_t *g, int codes, int scales) const
+    {
+        r = Row{};
+        if (g != nullptr) load_row(r, g + codes + (tok & 15) * 64, g + scales + (tok & 15) * 8);
     }
 };
 
@@ -329,6 +355,17 @@ paged_attn_tc_kernel(const PagedAttnParams p)
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
                      :: "r"(smem_addr(&sm.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // ---- the first keys and values are asked for before the queries
+    const bool producer = warp >= 8 && warp < 12;
+    Feed feed;
+    Row k, v;
+    const uint8_t *g = nullptr;
+    if (producer) {
+        feed.start(p, b, head, lo, hi, threadIdx.x - 8 * 32);
+        g = feed.step(p);
+        feed.load(k, g, kKVCodesK, kKVScalesK);
+        feed.load(v, g, kKVCodesV, kKVScalesV);
     }
     // ---- queries: a thread a row, times a power of two for bf16
     float scale = 0.0f;
@@ -433,36 +470,10 @@ paged_attn_tc_kernel(const PagedAttnParams p)
         int none = 0;
         if (lead) mma_commit(bars.drained);
         warp_wait(bars.drained, 0, &none);
-    } else if (warp >= 8) {
+    } else if (producer) {
         // ---------------------------------------------------------- keys and values
-        const int tok = threadIdx.x - 8 * 32;  // of the tile
-        const int32_t *table = p.table + (int64_t)b * p.table_stride;
-        const int pages = 8 / p.groups, rest = 8 - pages * p.groups, in_group = tok & 15;  // lo: a multiple of 16
-        const uint8_t *k_pool = p.pool + (int64_t)head * p.groups * kKVGroupBytes + in_group * 64;
-        const int64_t page_bytes = (int64_t)p.hk * p.groups * kKVGroupBytes;
-        Place place(lo + tok, p.groups);
-        // page ids a tile further ahead than the codes (-1: no such token)
-        int in = place.in, id = place.at < hi ? ld_s32(table + place.page) : -1;
-        auto step = [&]() -> const uint8_t * {  // the next tile's row
-            const uint8_t *at = id < 0 || id >= p.num_pages ? nullptr : k_pool + id * page_bytes + in * kKVGroupBytes;
-            place.next(p.groups, pages, rest);
-            in = place.in;
-            id = place.at < hi ? ld_s32(table + place.page) : -1;
-            return at;
-        };
-        auto load_k = [&](Row &x, const uint8_t *at) {
-            x = Row{};
-            if (at != nullptr) load_row(x, at + kKVCodesK, at + kKVScalesK - in_group * 56);
-        };
-        auto load_v = [&](Row &x, const uint8_t *at) {
-            x = Row{};
-            if (at != nullptr) load_row(x, at + kKVCodesV, at + kKVScalesV - in_group * 56);
-        };
+        const int tok = feed.tok;
         const uint32_t to = smem_addr(smem) + tok * 128 + ((tok & 7) << 4);
-        Row k, v;
-        const uint8_t *g = step();
-        load_k(k, g);
-        load_v(v, g);
         for (int j = 0; j < n; ++j) {
             const int st = j & 1;
             if (j >= 2 && !warp_wait(bars.k_empty + 8 * st, ((j >> 1) + 1) & 1, failed)) break;
@@ -472,14 +483,14 @@ paged_attn_tc_kernel(const PagedAttnParams p)
             async_proxy_fence();
             __syncwarp();
             if (lane == 0) bar_arrive(bars.k_full + 8 * st);
-            g = step();
-            load_k(k, g);
+            g = feed.step(p);
+            feed.load(k, g, kKVCodesK, kKVScalesK);
             if (j >= 2 && !warp_wait(bars.v_empty + 8 * st, ((j >> 1) + 1) & 1, failed)) break;
             decode_row(v, to + kV + st * kTileBytes);
             async_proxy_fence();
             __syncwarp();
             if (lane == 0) bar_arrive(bars.v_full + 8 * st);
-            load_v(v, g);
+            feed.load(v, g, kKVCodesV, kKVScalesV);
         }
     } else {
         // ---------------------------------------------------------- softmax
