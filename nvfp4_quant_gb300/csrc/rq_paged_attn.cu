@@ -168,11 +168,11 @@ __device__ __forceinline__ int query_of(const PagedAttnParams &p, const Seq &s, 
 // Stores 8 NT columns' results: out (and lse) of column col from its sums.
 template <typename DT, int VALS>
 __device__ __forceinline__ void store_out(const PagedAttnParams &p, const Seq &s, int head, int col,
-                                          int d0, float (&v)[VALS], float m, float l)
+                                          int d0, float (&v)[VALS], float m, float l, float v_gs)
 {
     const int i = query_of(p, s, col), h = head * p.per + col - i * p.per;
     const int64_t row = ((int64_t)(s.q0 + i) * p.hq + h);
-    const float inv = out_factor(p, l);
+    const float inv = out_factor(l, v_gs);
     uint8_t *dst = static_cast<uint8_t *>(p.out) + (row * 128 + d0) * 2;
 #pragma unroll
     for (int k = 0; k < VALS; k += 4)
@@ -254,7 +254,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
     const uint32_t vread = ring + kKVCodesV + c * 64 + (((g >> 1) ^ ((c >> 1) & 1) * 2) * 16) + (g & 1) * 8;
     const uint32_t ksread = ring + kKVScalesK + tok_of_row(g) * 8 + 2 * c;
     const uint32_t vsread = ring + kKVScalesV + c * 8 + g;
-    const float inv_kgs = 1.0f / ld_f32(p.k_gs);
+    const float inv_kgs = 1.0f / ld_f32(p.k_gs), v_gs = ld_f32(p.v_gs);
 
     Seq s = load_seq(p, b);
     Cut ct = cut<NT>(p, s);
@@ -588,7 +588,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
                 for (int k = 0; k < kVals; ++k) v[k] = fmaf(f, src[k], v[k]);
             }
             if (ntile == ct.tiles) {
-                store_out<DT, kVals>(p, s, head, col0 + col, d0, v, top, sum);
+                store_out<DT, kVals>(p, s, head, col0 + col, d0, v, top, sum, v_gs);
             } else {
                 float *part = parts + (tile0 == 0 ? kPartFloats<NT> : 0);
 #pragma unroll
@@ -631,6 +631,7 @@ paged_attn_join_kernel(const PagedAttnParams p, int ctas)
         return parts + ((int64_t)(i + k) * 2 + (k == 0)) * kPartFloats<NT>;
     };
     const Seq s = load_seq(p, me.seq);
+    const float v_gs = ld_f32(p.v_gs);
     const int lane = threadIdx.x & 31, d0 = lane * 4;
     for (int col = threadIdx.x >> 5; col < 8 * NT; col += 8) {
         const int at = me.block * 8 * NT + col;
@@ -660,7 +661,7 @@ paged_attn_join_kernel(const PagedAttnParams p, int ctas)
                 v[3] = fmaf(w, a[k].w, v[3]);
             }
         }
-        store_out<DT, 4>(p, s, me.head, at, d0, v, top, sum);
+        store_out<DT, 4>(p, s, me.head, at, d0, v, top, sum, v_gs);
     }
 }
 

@@ -69,9 +69,9 @@ __device__ __forceinline__ float2 row_power(float largest)
 }
 
 // Factor of O for the output row: 1 / (l gs_v), 0 where no key was seen.
-__device__ __forceinline__ float out_factor(const PagedAttnParams &p, float l)
+__device__ __forceinline__ float out_factor(float l, float v_gs)
 {
-    return l > 0.0f ? 1.0f / (l * ld_f32(p.v_gs)) : (l == 0.0f ? 0.0f : l);
+    return l > 0.0f ? 1.0f / (l * v_gs) : (l == 0.0f ? 0.0f : l);
 }
 
 __device__ __forceinline__ float lse_of(float m, float l)

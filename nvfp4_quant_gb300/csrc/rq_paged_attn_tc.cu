@@ -184,12 +184,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, failed));
 }
 
-// Byte of chunk c (8 channels, 0-15) of row r in a 32 KB operand tile.
-__device__ __forceinline__ uint32_t tile_at(int r, int c)
-{
-    return (uint32_t)(c >> 3) * (kTileBytes / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-}
-
 // Row tiles of the sequence for this kernel.
 __device__ __forceinline__ int row_blocks(const PagedAttnParams &p, const Seq &s)
 {
@@ -197,10 +191,12 @@ __device__ __forceinline__ int row_blocks(const PagedAttnParams &p, const Seq &s
     return rows > p.few ? (rows + kRows - 1) / kRows : 0;
 }
 
-// A key or value row of a tile: 64 bytes of codes and 8 scales in registers.
+// A key or value row of a tile: 64 bytes of codes and 8 scales in registers,
+// and whether it is one (else its values are 0).
 struct Row {
     uint4 c[4];
     uint2 f;
+    bool there;
 };
 
 __device__ __forceinline__ void load_row(Row &r, const uint8_t *codes, const uint8_t *scales)
@@ -218,7 +214,7 @@ __device__ __forceinline__ void decode_row(const Row &r, uint32_t to)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t w[4] = {r.c[i].x, r.c[i].y, r.c[i].z, r.c[i].w};
-        const uint32_t two = e4m3_pair(((i & 2) ? r.f.y : r.f.x) >> ((i & 1) * 16));
+        const uint32_t two = e4m3_pair((r.there ? ((i & 2) ? r.f.y : r.f.x) : 0u) >> ((i & 1) * 16));
         const uint32_t f[2] = {__byte_perm(two, two, 0x1010), __byte_perm(two, two, 0x3232)};
         uint32_t x[16];
 #pragma unroll
@@ -246,7 +242,8 @@ struct Feed {
     const uint8_t *pool;
     int64_t page_bytes;
 
-    __device__ __forceinline__ int page_id() const { return at < hi ? ld_s32(table + page) : -1; }
+    // of the token, or of the sequence's first page where it has none
+    __device__ __forceinline__ int page_id() const { return ld_s32(table + (at < hi ? page : 0)); }
 
     __device__ __forceinline__ void start(const PagedAttnParams &p, int seq, int head, int lo, int hi_, int tok_)
     {
@@ -263,10 +260,13 @@ struct Feed {
         id = page_id();
     }
 
-    // The group of the tile's token (null: none that can be read); on to the next tile.
-    __device__ __forceinline__ const uint8_t *step(const PagedAttnParams &p)
+    // The group of the tile's token, or, where there is none that can be read,
+    // of other memory (a load under a condition would be waited for at once);
+    // on to the next tile.
+    __device__ __forceinline__ const uint8_t *step(const PagedAttnParams &p, bool &there)
     {
-        const uint8_t *g = id < 0 || id >= p.num_pages ? nullptr : pool + id * page_bytes + in * kKVGroupBytes;
+        there = at < hi && id >= 0 && id < p.num_pages;
+        const uint8_t *g = there ? pool + id * page_bytes + in * kKVGroupBytes : p.workspace;
         at += kTile;
         page += pages;
         in += rest;
@@ -278,10 +278,10 @@ struct Feed {
         return g;
     }
 
-    __device__ __forceinline__ void load(Row &r, const uint8_t *g, int codes, int scales) const
+    __device__ __forceinline__ void load(Row &r, const uint8_t *g, bool there, int codes, int scales) const
     {
-        r = Row{};
-        if (g != nullptr) load_row(r, g + codes + (tok & 15) * 64, g + scales + (tok & 15) * 8);
+        load_row(r, g + codes + (tok & 15) * 64, g + scales + (tok & 15) * 8);
+        r.there = there;
     }
 };
 
@@ -360,52 +360,71 @@ paged_attn_tc_kernel(const PagedAttnParams p)
     const bool producer = warp >= 8 && warp < 12;
     Feed feed;
     Row k, v;
-    const uint8_t *g = nullptr;
-    if (producer) {
-        feed.start(p, b, head, lo, hi, threadIdx.x - 8 * 32);
-        g = feed.step(p);
-        feed.load(k, g, kKVCodesK, kKVScalesK);
-        feed.load(v, g, kKVCodesV, kKVScalesV);
-    }
-    // ---- queries: a thread a row, times a power of two for bf16
+    // ---- queries: a warp its 32 rows, 16 lanes a row and all loads at once (a
+    // thread a row took 5.8 us here), times a power of two for bf16
     float scale = 0.0f;
     const int t = warp >> 2, r = threadIdx.x & 127;  // tile and row (warps 0-7)
     const int row = t * kTile + r;                   // of the block
-    const int query = (row0 + row) / p.per;
-    const int64_t out_row = (int64_t)(s.q0 + query) * p.hq + head * p.per + (row0 + row) % p.per;
-    if (warp < 8) {
-        uint8_t *tile = smem + kQ + t * kTileBytes;
-        const uint8_t *src = static_cast<const uint8_t *>(p.q) +
-                             ((s.q0 + query) * p.q_stride + (int64_t)(head * p.per + (row0 + row) % p.per) * kD) * 2;
-        const bool real = row < rows;
-        float f = 1.0f, back = 1.0f;
-        if (std::is_same<DT, BF16>::value && real) {
-            float a = 0.0f;
-#pragma unroll 4
-            for (int c = 0; c < 16; ++c) {
-                float e[8];
-                unpack8<DT>(ld_keep16(src + 16 * c), e);
+    const int query = (row0 + row) / p.per, group_head = head * p.per + (row0 + row) - query * p.per;
+    const int64_t out_row = (int64_t)(s.q0 + query) * p.hq + group_head;
+    const bool real = row < rows;
+    if (producer && n > 0) {  // (the branches are one, so that neither keeps registers for the other)
+        bool there;
+        feed.start(p, b, head, lo, hi, threadIdx.x - 8 * 32);
+        const uint8_t *g = feed.step(p, there);
+        feed.load(k, g, there, kKVCodesK, kKVScalesK);
+        feed.load(v, g, there, kKVCodesV, kKVScalesV);
+    } else if (warp < 8) {
+        // rows past the last repeat the block's first one (a load under a
+        // condition would be waited for at once)
+        const int first_query = row0 / p.per, first_head = head * p.per + row0 - first_query * p.per;
+        const int64_t mine = (s.q0 + (real ? query : first_query)) * p.q_stride +
+                             (int64_t)(real ? group_head : first_head) * kD;
+        uint4 x[16];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) a = fmaxf(a, fabsf(e[k]));
+        for (int i = 0; i < 16; ++i) {
+            const int64_t at = __shfl_sync(0xFFFFFFFFu, mine, 2 * i + (lane >> 4));
+            x[i] = ld_keep16(static_cast<const uint8_t *>(p.q) + at * 2 + (lane & 15) * 16);
+        }
+        float back = 1.0f;  // of the thread's own row
+        if (std::is_same<DT, BF16>::value) {
+            // largest magnitudes, four rows' reductions side by side: bf16 bits
+            // without the sign order as the values
+#pragma unroll
+            for (int i0 = 0; i0 < 16; i0 += 4) {
+                uint32_t a[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 w = x[i0 + i];
+                    a[i] = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                    __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) a[i] = __vmaxu2(a[i], __shfl_xor_sync(0xFFFFFFFFu, a[i], o));
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 pw = row_power(__uint_as_float(max(a[i] << 16, a[i] & 0xFFFF0000u)));
+                    float e[8];
+                    unpack8<DT>(x[i0 + i], e);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) e[k] *= pw.x;
+                    x[i0 + i] = pack8<FP16>(e);
+                    const float other = __shfl_sync(0xFFFFFFFFu, pw.y, (lane & 1) * 16);
+                    back = (lane >> 1) == i0 + i ? other : back;
+                }
             }
-            const float2 pw = row_power(a);
-            f = pw.x;
-            back = pw.y;
+        }
+        const uint32_t tile = smem_addr(smem) + kQ + t * kTileBytes + ((lane >> 3) & 1) * (kTileBytes / 2);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int to = (warp & 3) * 32 + 2 * i + (lane >> 4);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                         :: "r"(tile + to * 128 + (((lane & 7) ^ (to & 7)) << 4)), "r"(x[i].x), "r"(x[i].y),
+                            "r"(x[i].z), "r"(x[i].w) : "memory");
         }
         scale = fmaxf(p.scale * back / ld_f32(p.k_gs), kLeastScale);
-#pragma unroll 4
-        for (int c = 0; c < 16; ++c) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (real) v = ld_keep16(src + 16 * c);
-            if (std::is_same<DT, BF16>::value) {
-                float e[8];
-                unpack8<DT>(v, e);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) e[k] *= f;
-                v = pack8<FP16>(e);
-            }
-            sts16(tile + tile_at(r, c), v);
-        }
         async_proxy_fence();
     }
     tm_fence_before();
@@ -477,28 +496,29 @@ paged_attn_tc_kernel(const PagedAttnParams p)
         for (int j = 0; j < n; ++j) {
             const int st = j & 1;
             if (j >= 2 && !warp_wait(bars.k_empty + 8 * st, ((j >> 1) + 1) & 1, failed)) break;
-            const uint32_t seen = __ballot_sync(0xFFFFFFFFu, g != nullptr);
+            const uint32_t seen = __ballot_sync(0xFFFFFFFFu, k.there);
             if (lane == 0) sm.seen[j & 3][warp - 8] = seen;
             decode_row(k, to + kK + st * kTileBytes);
             async_proxy_fence();
             __syncwarp();
             if (lane == 0) bar_arrive(bars.k_full + 8 * st);
-            g = feed.step(p);
-            feed.load(k, g, kKVCodesK, kKVScalesK);
+            bool there;
+            const uint8_t *g = feed.step(p, there);
+            feed.load(k, g, there, kKVCodesK, kKVScalesK);
             if (j >= 2 && !warp_wait(bars.v_empty + 8 * st, ((j >> 1) + 1) & 1, failed)) break;
             decode_row(v, to + kV + st * kTileBytes);
             async_proxy_fence();
             __syncwarp();
             if (lane == 0) bar_arrive(bars.v_full + 8 * st);
-            feed.load(v, g, kKVCodesV, kKVScalesV);
+            feed.load(v, g, there, kKVCodesV, kKVScalesV);
         }
     } else {
         // ---------------------------------------------------------- softmax
         const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's 32 rows
         const uint32_t s_at = at + kColS + t * 128, o_at = at + kColO + t * 128;
-        const bool real = row < rows;
         const int row_hi = real ? s.first_pos + query + 1 : 0;               // keys [row_lo, row_hi)
         const int row_lo = p.window > 0 ? row_hi - p.window : 0;
+        const float v_gs = ld_f32(p.v_gs);
         float m = kNoMax, l = 0.0f;
         for (int j = 0; j < n; ++j) {
             if (!warp_wait(bars.s_full + 8 * (t), j & 1, failed)) break;
@@ -556,8 +576,8 @@ paged_attn_tc_kernel(const PagedAttnParams p)
                 tm_wait_ld(x1);
                 exps(x1, 3);
             };
-            all_exps();
-            if (__any_sync(0xFFFFFFFFu, sum[0] + sum[1] + sum[2] + sum[3] > kPMax)) {
+            if (j > 0) all_exps();  // (the first tile has no maximum yet)
+            if (j == 0 || __any_sync(0xFFFFFFFFu, sum[0] + sum[1] + sum[2] + sum[3] > kPMax)) {
                 // a row's maximum has risen: take it, rescale, and form P again
                 float top = m;
 #pragma unroll 1
@@ -602,26 +622,43 @@ paged_attn_tc_kernel(const PagedAttnParams p)
             warp_wait(bars.pv_done + 8 * (t), (n - 1) & 1, failed);
             tm_fence_after();
         }
-        const float inv = *failed ? __uint_as_float(0x7FC00000u) : out_factor(p, l);
-        uint8_t *dst = static_cast<uint8_t *>(p.out) + out_row * (kD * 2);
-#pragma unroll 1
+        // through the tile's place of Q, so that a row's 256 bytes leave together
+        const bool bad = *failed;
+        const float inv = bad ? __uint_as_float(0x7FC00000u) : out_factor(l, v_gs);
+        const uint32_t tile = smem_addr(smem) + kQ + t * kTileBytes;
+#pragma unroll
         for (int c = 0; c < 4; ++c) {
             uint32_t x[32] = {};
             if (n > 0) {
                 tm_load32(o_at + 32 * c, x);
                 tm_wait_ld(x);
             }
-            if (real) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    float e[8];
+            for (int k = 0; k < 32; k += 8) {
+                float e[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) e[i] = l == 0.0f && !*failed ? 0.0f : __uint_as_float(x[k + i]) * inv;
-                    st16(dst + 64 * c + 2 * k, pack8<DT>(e));
-                }
+                for (int i = 0; i < 8; ++i) e[i] = l == 0.0f && !bad ? 0.0f : __uint_as_float(x[k + i]) * inv;
+                const uint4 v = pack8<DT>(e);
+                const int chunk = 4 * c + k / 8;
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                             :: "r"(tile + (chunk >> 3) * (kTileBytes / 2) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4)),
+                                "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
             }
         }
-        if (real && p.lse != nullptr) p.lse[out_row] = *failed ? __uint_as_float(0x7FC00000u) : lse_of(m, l);
+        __syncwarp();
+        const int64_t mine = real ? out_row : -1;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int64_t to = __shfl_sync(0xFFFFFFFFu, mine, 2 * i + (lane >> 4));
+            const int from = (warp & 3) * 32 + 2 * i + (lane >> 4);
+            uint4 v;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(tile + ((lane >> 3) & 1) * (kTileBytes / 2) + from * 128 +
+                               (((lane & 7) ^ (from & 7)) << 4)) : "memory");
+            if (to >= 0) st16(static_cast<uint8_t *>(p.out) + to * (kD * 2) + (lane & 15) * 16, v);
+        }
+        if (real && p.lse != nullptr) p.lse[out_row] = bad ? __uint_as_float(0x7FC00000u) : lse_of(m, l);
     }
     // ---------------------------------------------------------------- leave
     tm_fence_before();
