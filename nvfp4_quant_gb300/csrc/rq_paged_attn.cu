@@ -254,7 +254,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
     const uint32_t vread = ring + kKVCodesV + c * 64 + (((g >> 1) ^ ((c >> 1) & 1) * 2) * 16) + (g & 1) * 8;
     const uint32_t ksread = ring + kKVScalesK + tok_of_row(g) * 8 + 2 * c;
     const uint32_t vsread = ring + kKVScalesV + c * 8 + g;
-    const float inv_kgs = 1.0f / ld_f32(p.k_gs), v_gs = ld_f32(p.v_gs);
+    const float inv_kgs = 1.0f / ld_f32(p.k_gs);
 
     Seq s = load_seq(p, b);
     Cut ct = cut<NT>(p, s);
@@ -287,19 +287,36 @@ paged_attn_split_kernel(const PagedAttnParams p)
                                ? (t1 - t0 - warp * kChunk + kWarps * kChunk - 1) / (kWarps * kChunk)
                                : 0;  // of this warp
 
+        // ---- queries' loads: columns nt * 8 + g (past the last: the first
+        // again; a load under a condition would be waited for at once),
+        // channels 32 c .. + 31
+        uint4 qv[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int col = col0 + (nt * 8 + g < cols ? nt * 8 + g : 0);
+            const int i = query_of(p, s, col), h = head * p.per + col - i * p.per;
+            const uint8_t *src =
+                static_cast<const uint8_t *>(p.q) + ((s.q0 + i) * p.q_stride + (int64_t)h * 128 + 32 * c) * 2;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) qv[nt][k] = ld_keep16(src + 16 * k);
+        }
+
         // ---- groups of the warp's chunks, 32 groups at a time: lane kChunkGroups
         // i + j holds where group j of chunk i lies in the cache (-1: nowhere)
+        auto token_of = [&](int batch) {
+            return t0 + (warp + kWarps * (batch * kBatch + lane / kChunkGroups)) * kChunk + lane % kChunkGroups * 16;
+        };
+        // the page id of the batch's token, or of the part's first token where
+        // it has none; and the place, once the id is there
         auto find = [&](int batch) {
-            const int token = t0 + (warp + kWarps * (batch * kBatch + lane / kChunkGroups)) * kChunk +
-                              lane % kChunkGroups * 16;
-            int at = -1;
-            if (token < t1) {
-                const int slot = token >> 4, page = slot / p.groups;
-                const int id = ld_s32(p.table + (int64_t)b * p.table_stride + page);
-                if (id >= 0 && id < p.num_pages)
-                    at = (int)(((int64_t)id * p.hk + head) * p.groups + (slot - page * p.groups));
-            }
-            return at;
+            const int token = token_of(batch);
+            return ld_s32(p.table + (int64_t)b * p.table_stride + ((token < t1 ? token : t0) >> 4) / p.groups);
+        };
+        auto place = [&](int batch, int id) {
+            const int token = token_of(batch), slot = token >> 4;
+            return token < t1 && id >= 0 && id < p.num_pages
+                       ? (int)(((int64_t)id * p.hk + head) * p.groups + slot % p.groups)
+                       : -1;
         };
         auto fetch = [&](int i, int from, uint32_t stage) {  // starts the copies of chunk i
 #pragma unroll
@@ -317,26 +334,24 @@ paged_attn_split_kernel(const PagedAttnParams p)
             }
             cp_async_commit();
         };
-        int near = find(0), far = find(1);
+        int near_id = -1, far_id = -1;
+        if (t1 > t0) {
+            near_id = find(0);
+            far_id = find(1);
+        }
+        int near = place(0, near_id);
         for (int i = 0; i < kStages - 1; ++i) fetch(i, near, i * kChunkBytes);
         uint32_t near_ok = __ballot_sync(0xFFFFFFFFu, near >= 0);
+        int far = -1;  // from the chunk on whose fetch needs it
         uint32_t stage = 0, filled = (kStages - 1) * kChunkBytes;  // of chunk it, of the next to fetch
 
-        // ---- queries: columns nt * 8 + g, channels 32 c .. + 31, as the B
-        // operand; each row by a power of two so that fp16 holds it
+        // ---- queries as the B operand; each row by a power of two so that fp16
+        // holds it
         uint32_t qf[NT][16];
         float cs[NT][2], m[NT][2], l[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const int col = nt * 8 + g;
-            uint4 v[4] = {};
-            if (col < cols) {
-                const int i = query_of(p, s, col0 + col), h = head * p.per + col0 + col - i * p.per;
-                const uint8_t *src = static_cast<const uint8_t *>(p.q) +
-                                     ((s.q0 + i) * p.q_stride + (int64_t)h * 128 + 32 * c) * 2;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = ld_keep16(src + 16 * k);
-            }
+            uint4 (&v)[4] = qv[nt];
             float f = 1.0f, back = 1.0f;
             if (std::is_same<DT, BF16>::value) {
                 float a = 0.0f;
@@ -386,43 +401,52 @@ paged_attn_split_kernel(const PagedAttnParams p)
             __syncwarp();  // everyone's copies have landed; everyone is done with the stage before
             if (it > 0 && it % kBatch == 0) {
                 near = far;
-                far = find(it / kBatch + 1);
+                far_id = find(it / kBatch + 1);
                 near_ok = __ballot_sync(0xFFFFFFFFu, near >= 0);
             }
+            if (it % kBatch == kBatch - kStages + 1) far = place(it / kBatch + 1, far_id);
             fetch(it + kStages - 1, it % kBatch + kStages - 1 < kBatch ? near : far, filled);
             const int tok0 = t0 + (warp + kWarps * it) * kChunk;
             const uint32_t here = near_ok >> (it % kBatch * kChunkGroups);  // bit gr: the group is readable
             const bool full = tok0 >= need_lo && tok0 + kChunk <= need_hi && (here & kAll) == kAll;
 
-            // ---- S^T = K Q^T
+            // ---- S^T = K Q^T, the two groups' chains of products side by side
             float x[kChunkGroups][NT][4];
+            uint4 ka[kChunkGroups], kb[kChunkGroups];
+            uint32_t sa[kChunkGroups], sb[kChunkGroups];
 #pragma unroll
             for (int gr = 0; gr < kChunkGroups; ++gr) {
                 const uint32_t base = stage + gr * kKVGroupBytes;
-                const uint4 ka = lds16_at<0>(base + kread), kb = lds16_at<512>(base + kread);
-                const uint32_t sa = e4m3_pair(lds2_at<0>(base + ksread));
-                const uint32_t sb = e4m3_pair(lds2_at<64>(base + ksread));
-                const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+                ka[gr] = lds16_at<0>(base + kread);
+                kb[gr] = lds16_at<512>(base + kread);
+                sa[gr] = lds2_at<0>(base + ksread);
+                sb[gr] = lds2_at<64>(base + ksread);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[gr][nt][e] = 0.0f;
+            }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t fa = __byte_perm(sa, sa, k < 2 ? 0x1010 : 0x3232);
-                    const uint32_t fb = __byte_perm(sb, sb, k < 2 ? 0x1010 : 0x3232);
-                    const uint32_t a0 = FP16::mul2(e2m1_pair<0>(wa[k]), fa);
-                    const uint32_t a1 = FP16::mul2(e2m1_pair<0>(wb[k]), fb);
-                    const uint32_t a2 = FP16::mul2(e2m1_pair<1>(wa[k]), fa);
-                    const uint32_t a3 = FP16::mul2(e2m1_pair<1>(wb[k]), fb);
-                    const uint32_t a4 = FP16::mul2(e2m1_pair<2>(wa[k]), fa);
-                    const uint32_t a5 = FP16::mul2(e2m1_pair<2>(wb[k]), fb);
-                    const uint32_t a6 = FP16::mul2(e2m1_pair<3>(wa[k]), fa);
-                    const uint32_t a7 = FP16::mul2(e2m1_pair<3>(wb[k]), fb);
+            for (int gr = 0; gr < kChunkGroups; ++gr) {
+                sa[gr] = e4m3_pair(sa[gr]);
+                sb[gr] = e4m3_pair(sb[gr]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                for (int gr = 0; gr < kChunkGroups; ++gr) {
+                    const uint32_t wa = k == 0 ? ka[gr].x : k == 1 ? ka[gr].y : k == 2 ? ka[gr].z : ka[gr].w;
+                    const uint32_t wb = k == 0 ? kb[gr].x : k == 1 ? kb[gr].y : k == 2 ? kb[gr].z : kb[gr].w;
+                    const uint32_t fa = __byte_perm(sa[gr], sa[gr], k < 2 ? 0x1010 : 0x3232);
+                    const uint32_t fb = __byte_perm(sb[gr], sb[gr], k < 2 ? 0x1010 : 0x3232);
+                    uint32_t u[8] = {e2m1_pair<0>(wa), e2m1_pair<0>(wb), e2m1_pair<1>(wa), e2m1_pair<1>(wb),
+                                     e2m1_pair<2>(wa), e2m1_pair<2>(wb), e2m1_pair<3>(wa), e2m1_pair<3>(wb)};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) u[i] = FP16::mul2(u[i], i & 1 ? fb : fa);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma(x[gr][nt], a0, a1, a2, a3, qf[nt][4 * k], qf[nt][4 * k + 1]);
-                        mma(x[gr][nt], a4, a5, a6, a7, qf[nt][4 * k + 2], qf[nt][4 * k + 3]);
+                        mma(x[gr][nt], u[0], u[1], u[2], u[3], qf[nt][4 * k], qf[nt][4 * k + 1]);
+                        mma(x[gr][nt], u[4], u[5], u[6], u[7], qf[nt][4 * k + 2], qf[nt][4 * k + 3]);
                     }
                 }
             }
@@ -536,24 +560,25 @@ paged_attn_split_kernel(const PagedAttnParams p)
                     const uint32_t lo = 0x0F0F0F0Fu;
                     const uint32_t ea = (w0 & lo) | ((w1 << 4) & ~lo), oa = ((w0 >> 4) & lo) | (w1 & ~lo);
                     const uint32_t eb = (w2 & lo) | ((w3 << 4) & ~lo), ob = ((w2 >> 4) & lo) | (w3 & ~lo);
-#define RQ_PV(B)                                                                                     \
-    {                                                                                                \
-        const uint32_t a0 = FP16::mul2(e2m1_pair<B>(ea), sa), a1 = FP16::mul2(e2m1_pair<B>(oa), sa); \
-        const uint32_t a2 = FP16::mul2(e2m1_pair<B>(eb), sb), a3 = FP16::mul2(e2m1_pair<B>(ob), sb); \
-        _Pragma("unroll") for (int nt = 0; nt < NT; ++nt)                                            \
-            mma(o[nt][4 * k + B], a0, a1, a2, a3, pf[gr][nt][0], pf[gr][nt][1]);                     \
-    }
-                    RQ_PV(0)
-                    RQ_PV(1)
-                    RQ_PV(2)
-                    RQ_PV(3)
-#undef RQ_PV
+                    uint32_t u[16] = {e2m1_pair<0>(ea), e2m1_pair<0>(oa), e2m1_pair<0>(eb), e2m1_pair<0>(ob),
+                                      e2m1_pair<1>(ea), e2m1_pair<1>(oa), e2m1_pair<1>(eb), e2m1_pair<1>(ob),
+                                      e2m1_pair<2>(ea), e2m1_pair<2>(oa), e2m1_pair<2>(eb), e2m1_pair<2>(ob),
+                                      e2m1_pair<3>(ea), e2m1_pair<3>(oa), e2m1_pair<3>(eb), e2m1_pair<3>(ob)};
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) u[i] = FP16::mul2(u[i], i & 2 ? sb : sa);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma(o[nt][4 * k + i], u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3], pf[gr][nt][0],
+                                pf[gr][nt][1]);
                 }
             }
             stage = stage == (kStages - 1) * kChunkBytes ? 0 : stage + kChunkBytes;
             filled = filled == (kStages - 1) * kChunkBytes ? 0 : filled + kChunkBytes;
         }
 
+        const float v_gs = ld_f32(p.v_gs);
         // ---- join the warps: O of column k in the warp's ring, 512 bytes each
         cp_async_wait<0>();
         __syncwarp();
