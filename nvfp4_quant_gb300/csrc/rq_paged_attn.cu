@@ -729,7 +729,17 @@ cudaError_t launch_paged_attn(const PagedAttnParams &p, cudaStream_t stream)
     PagedAttnParams few = p;
     few.few = INT_MAX;
     if (cols <= 8) return launch_split<DT, 1>(few, dev, stream);
-    if (p.q_starts == nullptr || cols <= kFewColumns) return launch_split<DT, 2>(few, dev, stream);
+    // This kernel's time goes with blocks of 16 columns, spread over every SM;
+    // the tensor-memory kernel's with waves of 256-row blocks, each on one SM for
+    // all its keys.  Measured at 8 KV heads, 16-column blocks here against
+    // waves there: 1 sequence of 30,000 keys and 128, 256 and 512 columns 106,
+    // 197 and 381 us (396, 354 and 355 there); 4 of 8192 and 64, 128 and 256
+    // 66, 119 and 223 (125, 119 and 108); 32 of 2048 and 36, 48 and 64 88,
+    // 103 and 132 (81, 83 and 80): equal near 270 blocks a wave.
+    const int64_t rows = (int64_t)p.per * p.n_tokens, sms = device_sms(dev);
+    const int64_t blocks16 = (rows / 16 + p.n_seqs) * p.hk, blocks256 = (rows / 256 + p.n_seqs) * p.hk;
+    if (p.q_starts == nullptr || cols <= kFewColumns || blocks16 <= 270 * ((blocks256 + sms - 1) / sms))
+        return launch_split<DT, 2>(few, dev, stream);
     few.few = kFewColumns;
     e = launch_split<DT, 2>(few, dev, stream);
     return e != cudaSuccess ? e : launch_paged_attn_tc<DT>(few, stream);

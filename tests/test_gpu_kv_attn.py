@@ -253,6 +253,57 @@ def test_extend_prompts(hq, hk, page, dt, window):
     run_extend(Cache(10, lens, hk, page), hq, new, dt, window=window, behind=3)
 
 
+@pytest.mark.parametrize("window", [0, 60])
+@pytest.mark.parametrize("hq, hk, page, dt", [(16, 2, 16, "bf16"), (20, 4, 48, "fp16"), (8, 8, 32, "bf16"),
+                                              (48, 2, 64, "fp16")])
+def test_extend_mixed_batch(hq, hk, page, dt, window):
+    """A batch of single tokens, drafted runs, chunks and prompts: both of the
+    library's attention kernels take their part of it."""
+    r = np.random.default_rng(hq)
+    new = [1, 4, 90, 1, 0, 130, 257, 33, 1, 7, 300, 64, 2, 150]
+    old = r.integers(0, 400, len(new))
+    lens = [int(a + b) for a, b in zip(old, new)]
+    lens[5] = 100  # fewer keys than queries
+    run_extend(Cache(21, lens, hk, page), hq, new, dt, window=window, behind=2)
+
+
+def test_extend_prompts_of_many_heads():
+    run_extend(Cache(22, [128, 129, 500, 640], 4, 16), 32, [128, 129, 255, 300], "bf16")
+    run_extend(Cache(22, [700] * 9, 4, 64), 4, [200] * 9, "fp16", window=333)
+
+
+def test_extend_bad_pages_in_a_prompt():
+    """Unreadable pages in the middle of chunks whose rows fill several blocks."""
+    c = Cache(23, [900, 640], 2, 16)
+    table = c.table.copy()
+    table[0, [0, 7, 8, 9, 10, 11, 12, 13, 14, 15, 40]] = -1
+    table[1, :] = c.pages
+    out = run_extend(c, 32, [420, 333], "bf16", table=table)
+    assert not out[420:].any()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_extend_score_ranges(dt):
+    """As test_score_ranges, for chunks: rows without size, large and small
+    rows, keys that grow so that the maximum moves in every tile."""
+    c = Cache(24, [1000, 700], 2, 32)
+    k = np.zeros((1000, 2, D))
+    k[:, :, 7] = np.linspace(-9, 9, 1000)[:, None]
+    kc, ks = kv_ref.nvfp4(k, GS_K)
+    vc, vs = kv_ref.nvfp4(np.random.default_rng(5).standard_normal((1000, 2, D)), GS_V)
+    for t in range(1000):
+        for h in range(2):
+            kv_ref.store(c.pool, 32, int(c.table[0, t // 32]) * 32 + t % 32, h, kc[t, h], ks[t, h], vc[t, h], vs[t, h])
+    c.dpool.copy_(torch.from_numpy(c.pool))
+    f = pins.bits_to_f64(synth.normal_tensor(1, 4, (600, 16, D), dt), dt)
+    f[:200, :, 7] *= np.linspace(-60, 60, 200)[:, None]
+    f[200:260] *= 40.0
+    f[260:300] *= 2.0 ** -18
+    f[300:310] = 0
+    f[310:400, :, :100] *= 2.0 ** -16
+    run_extend(c, 16, [300, 300], dt, q=synth.to_bits(f, dt))
+
+
 def test_extend_long_chunk():
     run_extend(Cache(11, [3000], 1, 64), 4, [1100], "bf16")
     run_extend(Cache(11, [2500, 600], 2, 16), 4, [700, 600], "fp16", window=600)
