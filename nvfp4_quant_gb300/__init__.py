@@ -439,9 +439,11 @@ def rq_qk_rmsnorm_rope_fp8_dynamic(q, k, q_weight, k_weight, eps, positions, cos
 # These calls are short (a decode step's append runs for 4 us on the GPU), so
 # their checks are kept to the cheapest torch queries.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_I32, _I64, _F32, _U8 = torch.int32, torch.int64, torch.float32, torch.uint8
 
 
-def _same_device(*tensors):
+def _same_device(tensors):
     """The index of the device that every given tensor lies on."""
     dev = tensors[0].get_device()
     for t in tensors:
@@ -459,7 +461,7 @@ def _call_on(dev, fn, args, stream):
         stream = _raw_stream(dev) if _raw_stream else torch.cuda.current_stream(dev).cuda_stream
     else:
         stream = getattr(stream, "cuda_stream", stream)
-    if torch.cuda.current_device() == dev:
+    if _current_device() == dev:
         status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -470,7 +472,7 @@ def _call_on(dev, fn, args, stream):
 
 def _typed(t, dtype, numel, name):
     """A contiguous tensor of at least numel elements of a type."""
-    if t is None or t.dtype != dtype or t.numel() < numel or not t.is_contiguous():
+    if t is None or t.dtype is not dtype or t.numel() < numel or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of at least %d elements"
                          % (name, str(dtype).replace("torch.", ""), numel))
     return t.data_ptr()
@@ -478,7 +480,7 @@ def _typed(t, dtype, numel, name):
 
 def _cache(kv_pool, page_size, heads):
     shape = kv_pool.shape
-    if len(shape) != 3 or kv_pool.dtype != torch.uint8 or shape[1] != heads or \
+    if len(shape) != 3 or kv_pool.dtype is not _U8 or shape[1] != heads or \
             shape[2] != page_size * 144 or not kv_pool.is_contiguous():
         raise ValueError("kv_pool must be a contiguous uint8 [num_pages, n_kv_heads, page_size * 144] "
                          "tensor with %d heads" % heads)
@@ -504,8 +506,8 @@ def rq_qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos
     (include/rq.h).  q [T, Hq, 128], k, v [T, Hk, 128] may be token-strided
     views; q_out [T, Hq, 128]; kv_pool uint8 [pages, Hk, page_size * 144];
     slots int64 [T] (page * page_size + index; outside the cache: not stored)."""
-    dev = _same_device(q, k, v, q_weight, k_weight, positions, cos_sin_cache, k_global_scale,
-                       v_global_scale, q_out, kv_pool, slots)
+    dev = _same_device((q, k, v, q_weight, k_weight, positions, cos_sin_cache, k_global_scale,
+                        v_global_scale, q_out, kv_pool, slots))
     qp, qs = _head_rows(q, "q")
     kp, ks = _head_rows(k, "k", q)
     vp, vs = _head_rows(v, "v", q)
@@ -513,54 +515,53 @@ def rq_qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos
     hk = k.shape[1]
     if v.shape[1] != hk:
         raise ValueError("k and v must have the same heads")
+    dtype = q.dtype
     for w in (q_weight, k_weight):
-        if w is not None and (w.dtype != q.dtype or w.numel() != d or not w.is_contiguous()):
+        if w is not None and (w.dtype is not dtype or w.numel() != d or not w.is_contiguous()):
             raise ValueError("weights must be [head_dim] of q's dtype")
-    if cos_sin_cache.dtype != torch.float32 or cos_sin_cache.dim() != 2 or \
-            cos_sin_cache.shape[1] != d or not cos_sin_cache.is_contiguous():
+    table = cos_sin_cache.shape
+    if cos_sin_cache.dtype is not _F32 or len(table) != 2 or table[1] != d or \
+            not cos_sin_cache.is_contiguous():
         raise ValueError("cos_sin_cache must be a contiguous [max_pos, %d] float32 tensor" % d)
-    if q_out.dtype != q.dtype:
-        raise ValueError("q_out must have q's dtype")
     pool, pages, page = _cache(kv_pool, page_size, hk)
     _call_on(dev, lib().rq_qkv_rope_nvfp4_kv_append, (
         qp, kp, vp, qs, ks, vs, t, hq, hk, d, None if q_weight is None else q_weight.data_ptr(),
-        None if k_weight is None else k_weight.data_ptr(), float(eps),
-        _typed(positions, torch.int32, t, "positions"), cos_sin_cache.data_ptr(),
-        cos_sin_cache.shape[0], _typed(k_global_scale, torch.float32, 1, "k_global_scale"),
-        _typed(v_global_scale, torch.float32, 1, "v_global_scale"),
-        _typed(q_out, q.dtype, t * hq * d, "q_out"), pool, pages, page,
-        _typed(slots, torch.int64, t, "slots"), _dt(q)), stream)
+        None if k_weight is None else k_weight.data_ptr(), eps, _typed(positions, _I32, t, "positions"),
+        cos_sin_cache.data_ptr(), table[0], _typed(k_global_scale, _F32, 1, "k_global_scale"),
+        _typed(v_global_scale, _F32, 1, "v_global_scale"), _typed(q_out, dtype, t * hq * d, "q_out"),
+        pool, pages, page, _typed(slots, _I64, t, "slots"), _dt(q)), stream)
 
 
 def _paged_attn(q, kv_pool, page_size, block_table, q_starts, max_q_len, kv_lens, k_gs, v_gs,
                 sm_scale, out, workspace, window, lse, stream):
-    dev = _same_device(q, kv_pool, block_table, q_starts, kv_lens, k_gs, v_gs, out, workspace, lse)
+    dev = _same_device((q, kv_pool, block_table, q_starts, kv_lens, k_gs, v_gs, out, workspace, lse))
     qp, qs = _head_rows(q, "q")
     t, hq, d = q.shape
-    if kv_pool.dim() != 3 or kv_pool.shape[1] < 1 or hq % kv_pool.shape[1] != 0:
+    hk = kv_pool.shape[1] if kv_pool.dim() == 3 else 0
+    if hk < 1 or hq % hk != 0:
         raise ValueError("q's heads must be a multiple of the cache's")
-    hk = kv_pool.shape[1]
     pool, pages, page = _cache(kv_pool, page_size, hk)
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or \
-            (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be an int32 [n_seqs, pages_per_seq] tensor with contiguous rows")
+    if block_table.dtype is not _I32 or block_table.dim() != 2:
+        raise ValueError("block_table must be an int32 [n_seqs, pages_per_seq] tensor")
     n, per = block_table.shape
-    row = block_table.stride(0) if n > 1 else per
-    tail = (_typed(kv_lens, torch.int32, n, "kv_lens"), float(sm_scale), int(window),
-            _typed(k_gs, torch.float32, 1, "k_global_scale"),
-            _typed(v_gs, torch.float32, 1, "v_global_scale"), _typed(out, q.dtype, t * hq * d, "out"),
-            None if lse is None else _typed(lse, torch.float32, t * hq, "lse"), workspace.data_ptr(),
+    row, col = block_table.stride()
+    if col != 1 and per > 1:
+        raise ValueError("block_table's rows must be contiguous")
+    if n < 2:
+        row = per
+    tail = (_typed(kv_lens, _I32, n, "kv_lens"), sm_scale, window, _typed(k_gs, _F32, 1, "k_global_scale"),
+            _typed(v_gs, _F32, 1, "v_global_scale"), _typed(out, q.dtype, t * hq * d, "out"),
+            None if lse is None else _typed(lse, _F32, t * hq, "lse"), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), _dt(q))
-    L = lib()
     if q_starts is None:
         if t != n:
             raise ValueError("q must hold one query per sequence")
-        _call_on(dev, L.rq_paged_decode_attn_nvfp4, (
+        _call_on(dev, lib().rq_paged_decode_attn_nvfp4, (
             qp, qs, n, hq, hk, d, pool, pages, page, block_table.data_ptr(), row, per) + tail, stream)
     else:
-        _call_on(dev, L.rq_paged_extend_attn_nvfp4, (
-            qp, qs, t, _typed(q_starts, torch.int32, n + 1, "q_starts"), n, int(max_q_len), hq, hk, d,
-            pool, pages, page, block_table.data_ptr(), row, per) + tail, stream)
+        _call_on(dev, lib().rq_paged_extend_attn_nvfp4, (
+            qp, qs, t, _typed(q_starts, _I32, n + 1, "q_starts"), n, max_q_len, hq, hk, d, pool, pages,
+            page, block_table.data_ptr(), row, per) + tail, stream)
 
 
 def rq_paged_decode_attn_nvfp4(q, kv_pool, page_size, block_table, kv_lens, k_global_scale,
@@ -692,10 +693,10 @@ def qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos_si
     """Allocate q_out (torch) and run rq_qkv_rope_nvfp4_kv_append.  Returns
     q_out [T, Hq, 128]."""
     if stream is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     else:
         with _on_stream(stream, q.device):
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     rq_qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos_sin_cache,
                                 k_global_scale, v_global_scale, q_out, kv_pool, slots, page_size,
                                 stream)
@@ -706,11 +707,10 @@ def _attn_buffers(q, kv_pool, with_lse, workspace, stream):
     if stream is not None:
         with _on_stream(stream, q.device):
             return _attn_buffers(q, kv_pool, with_lse, workspace, None)
-    out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if with_lse else None
+    out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    lse = q.new_empty(q.shape[:2], dtype=_F32) if with_lse else None
     if workspace is None:
-        workspace = torch.empty((rq_paged_attn_nvfp4_workspace_bytes(q.shape[1], kv_pool.shape[1]),),
-                                dtype=torch.uint8, device=q.device)
+        workspace = q.new_empty((rq_paged_attn_nvfp4_workspace_bytes(q.shape[1], kv_pool.shape[1]),), dtype=_U8)
     return out, lse, workspace
 
 
@@ -720,8 +720,8 @@ def paged_decode_attn_nvfp4(q, kv_pool, page_size, block_table, kv_lens, k_globa
     """Allocate the outputs (and, unless given, the workspace) and run
     rq_paged_decode_attn_nvfp4.  Returns (out, lse or None)."""
     out, lse, workspace = _attn_buffers(q, kv_pool, with_lse, workspace, stream)
-    rq_paged_decode_attn_nvfp4(q, kv_pool, page_size, block_table, kv_lens, k_global_scale,
-                               v_global_scale, sm_scale, out, workspace, window, lse, stream)
+    _paged_attn(q, kv_pool, page_size, block_table, None, 1, kv_lens, k_global_scale,
+                v_global_scale, sm_scale, out, workspace, window, lse, stream)
     return out, lse
 
 
@@ -731,8 +731,9 @@ def paged_extend_attn_nvfp4(q, kv_pool, page_size, block_table, q_starts, kv_len
     """Allocate the outputs (and, unless given, the workspace) and run
     rq_paged_extend_attn_nvfp4.  Returns (out, lse or None); rows of out behind
     the last sequence are not written."""
+    if q_starts is None:
+        raise ValueError("q_starts must be an int32 [n_seqs + 1] tensor")
     out, lse, workspace = _attn_buffers(q, kv_pool, with_lse, workspace, stream)
-    rq_paged_extend_attn_nvfp4(q, kv_pool, page_size, block_table, q_starts, kv_lens, max_q_len,
-                               k_global_scale, v_global_scale, sm_scale, out, workspace, window, lse,
-                               stream)
+    _paged_attn(q, kv_pool, page_size, block_table, q_starts, max_q_len, kv_lens, k_global_scale,
+                v_global_scale, sm_scale, out, workspace, window, lse, stream)
     return out, lse
