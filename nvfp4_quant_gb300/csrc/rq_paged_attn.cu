@@ -56,6 +56,7 @@ constexpr int kSmem = kWarps * kStages * kChunkBytes;
 // Queries x heads of a KV head up to which a sequence is taken here and not by
 // the tensor-memory kernel.
 constexpr int kFewColumns = 32;
+constexpr int kCluster = 8, kParts = kCluster * kWarps;
 constexpr int kMaxCtas = 1024;     // grid limit (workspace slots)
 
 // A part: O [8 NT][128], m [8 NT], l [8 NT].
@@ -165,6 +166,26 @@ __device__ __forceinline__ int query_of(const PagedAttnParams &p, const Seq &s, 
     return s.nq == 1 ? 0 : (int)((uint32_t)col / (uint32_t)p.per);
 }
 
+// Barrier of the cluster; an address of another CTA's shared memory, and a load
+// from it.
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n"
+                 "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_addr(const void *mine, int rank)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(mine)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t a)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+
 // Stores 8 NT columns' results: out (and lse) of column col from its sums.
 template <typename DT, int VALS>
 __device__ __forceinline__ void store_out(const PagedAttnParams &p, const Seq &s, int head, int col,
@@ -182,11 +203,362 @@ __device__ __forceinline__ void store_out(const PagedAttnParams &p, const Seq &s
         p.lse[row] = lse_of(m, l);
 }
 
+// Where a lane's pieces of a group go in its warp's ring and where it reads them.
+struct WarpRing {
+    uint32_t kdst, vdst, fdst, kread, vread, ksread, vsread;
+    float *o;  // the same memory, for the warp's part of O at the end
+
+    __device__ __forceinline__ explicit WarpRing(uint8_t *mem)
+    {
+        const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+        const uint32_t ring = smem_addr(mem);
+        // the 16-byte pieces of a group (the fifth: lanes 0-15)
+        kdst = ring + row_of_tok(lane >> 2) * 64 + (lane & 3) * 16;  // + 512: tokens 8-15
+        vdst = ring + kKVCodesV + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 1) * 2) * 16);
+        fdst = ring + kKVScalesK + lane * 16;
+        kread = ring + g * 64 + c * 16;
+        vread = ring + kKVCodesV + c * 64 + (((g >> 1) ^ ((c >> 1) & 1) * 2) * 16) + (g & 1) * 8;
+        ksread = ring + kKVScalesK + tok_of_row(g) * 8 + 2 * c;
+        vsread = ring + kKVScalesV + c * 8 + g;
+        o = reinterpret_cast<float *>(mem);
+    }
+};
+
+// A warp's part of an item: columns col0 .. col0 + cols - 1 of a sequence and KV
+// head over the chunks first, first + step, .. of the keys from t0 (up to end
+// and to what the columns see).  Leaves O [8 NT][128] in the warp's ring and m
+// and the sum l of the columns in stats [8 NT].
+template <typename DT, int NT>
+__device__ __forceinline__ void attend(const PagedAttnParams &p, const Seq &s, int b, int head, int col0, int cols,
+                                       int t0, int end, int first, int step, float inv_kgs, const WarpRing &w,
+                                       float2 *stats)
+{
+    static_assert(kStages * kChunkBytes >= 8 * NT * 128 * 4, "a warp's ring holds its part of O at the end");
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    // keys that the block's columns see: all of [need_lo, need_hi) by every
+    // one, nothing from blk_hi on by any
+    const int i_first = query_of(p, s, col0), i_last = query_of(p, s, col0 + cols - 1);
+    const int blk_hi = s.first_pos + i_last + 1;
+    const int need_hi = s.first_pos + i_first + 1;
+    const int need_lo = p.window > 0 ? blk_hi - p.window : 0;
+    const int t1 = min(blk_hi, end);  // may lie before t0: nothing to do
+    const int chunks =
+        t1 > t0 + first * kChunk ? (t1 - t0 - first * kChunk + step * kChunk - 1) / (step * kChunk) : 0;
+
+    // ---- queries' loads: columns nt * 8 + g (past the last: the first
+    // again; a load under a condition would be waited for at once),
+    // channels 32 c .. + 31
+    uint4 qv[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int col = col0 + (nt * 8 + g < cols ? nt * 8 + g : 0);
+        const int i = query_of(p, s, col), h = head * p.per + col - i * p.per;
+        const uint8_t *src =
+            static_cast<const uint8_t *>(p.q) + ((s.q0 + i) * p.q_stride + (int64_t)h * 128 + 32 * c) * 2;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) qv[nt][k] = ld_keep16(src + 16 * k);
+    }
+
+    // ---- groups of the warp's chunks, 32 groups at a time: lane kChunkGroups
+    // i + j holds where group j of chunk i lies in the cache (-1: nowhere)
+    auto token_of = [&](int batch) {
+        return t0 + (first + step * (batch * kBatch + lane / kChunkGroups)) * kChunk + lane % kChunkGroups * 16;
+    };
+    // the page id of the batch's token, or of the part's first token where
+    // it has none; and the place, once the id is there
+    auto find = [&](int batch) {
+        const int token = token_of(batch);
+        return ld_s32(p.table + (int64_t)b * p.table_stride + ((token < t1 ? token : t0) >> 4) / p.groups);
+    };
+    auto place = [&](int batch, int id) {
+        const int token = token_of(batch), slot = token >> 4;
+        return token < t1 && id >= 0 && id < p.num_pages
+                   ? (int)(((int64_t)id * p.hk + head) * p.groups + slot % p.groups)
+                   : -1;
+    };
+    auto fetch = [&](int i, int from, uint32_t stage) {  // starts the copies of chunk i
+#pragma unroll
+        for (int gr = 0; gr < kChunkGroups; ++gr) {
+            const int at = __shfl_sync(0xFFFFFFFFu, from, i % kBatch * kChunkGroups + gr);
+            if (at >= 0 && i < chunks) {
+                const uint8_t *src = p.pool + (int64_t)at * kKVGroupBytes + lane * 16;
+                const uint32_t d = stage + gr * kKVGroupBytes;
+                cp16_at<0, 0>(d + w.kdst, src);
+                cp16_at<512, 512>(d + w.kdst, src);
+                cp16_at<0, 1024>(d + w.vdst, src);
+                cp16_at<512, 1536>(d + w.vdst, src);
+                if (lane < 16) cp16_at<0, 2048>(d + w.fdst, src);
+            }
+        }
+        cp_async_commit();
+    };
+    int near_id = -1, far_id = -1;
+    if (t1 > t0) {
+        near_id = find(0);
+        far_id = find(1);
+    }
+    int near = place(0, near_id);
+    for (int i = 0; i < kStages - 1; ++i) fetch(i, near, i * kChunkBytes);
+    uint32_t near_ok = __ballot_sync(0xFFFFFFFFu, near >= 0);
+    int far = -1;  // from the chunk on whose fetch needs it
+    uint32_t stage = 0, filled = (kStages - 1) * kChunkBytes;  // of chunk it, of the next to fetch
+
+    // ---- queries as the B operand; each row by a power of two so that fp16
+    // holds it
+    uint32_t qf[NT][16];
+    float cs[NT][2], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        uint4 (&v)[4] = qv[nt];
+        float f = 1.0f, back = 1.0f;
+        if (std::is_same<DT, BF16>::value) {
+            float a = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float e[8];
+                unpack8<DT>(v[k], e);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(e[j]));
+            }
+            a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
+            a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
+            const float2 pw = row_power(a);
+            f = pw.x;
+            back = pw.y;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (std::is_same<DT, BF16>::value) {
+                float e[8];
+                unpack8<DT>(v[k], e);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) e[j] *= f;
+                v[k] = pack8<FP16>(e);
+            }
+            qf[nt][4 * k] = v[k].x;
+            qf[nt][4 * k + 1] = v[k].y;
+            qf[nt][4 * k + 2] = v[k].z;
+            qf[nt][4 * k + 3] = v[k].w;
+        }
+        const float scale = fmaxf(p.scale * inv_kgs * back, kLeastScale);
+        cs[nt][0] = __shfl_sync(0xFFFFFFFFu, scale, 8 * c);
+        cs[nt][1] = __shfl_sync(0xFFFFFFFFu, scale, 8 * c + 4);
+        m[nt][0] = m[nt][1] = kNoMax;
+        l[nt][0] = l[nt][1] = 0.0f;
+    }
+    float o[NT][8][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.0f;
+
+    for (int it = 0; it < chunks; ++it) {
+        cp_async_wait<kStages - 2>();
+        __syncwarp();  // everyone's copies have landed; everyone is done with the stage before
+        if (it > 0 && it % kBatch == 0) {
+            near = far;
+            far_id = find(it / kBatch + 1);
+            near_ok = __ballot_sync(0xFFFFFFFFu, near >= 0);
+        }
+        if (it % kBatch == kBatch - kStages + 1) far = place(it / kBatch + 1, far_id);
+        fetch(it + kStages - 1, it % kBatch + kStages - 1 < kBatch ? near : far, filled);
+        const int tok0 = t0 + (first + step * it) * kChunk;
+        const uint32_t here = near_ok >> (it % kBatch * kChunkGroups);  // bit gr: the group is readable
+        const bool full = tok0 >= need_lo && tok0 + kChunk <= need_hi && (here & kAll) == kAll;
+
+        // ---- S^T = K Q^T, the two groups' chains of products side by side
+        float x[kChunkGroups][NT][4];
+        uint4 ka[kChunkGroups], kb[kChunkGroups];
+        uint32_t sa[kChunkGroups], sb[kChunkGroups];
+#pragma unroll
+        for (int gr = 0; gr < kChunkGroups; ++gr) {
+            const uint32_t base = stage + gr * kKVGroupBytes;
+            ka[gr] = lds16_at<0>(base + w.kread);
+            kb[gr] = lds16_at<512>(base + w.kread);
+            sa[gr] = lds2_at<0>(base + w.ksread);
+            sb[gr] = lds2_at<64>(base + w.ksread);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[gr][nt][e] = 0.0f;
+        }
+#pragma unroll
+        for (int gr = 0; gr < kChunkGroups; ++gr) {
+            sa[gr] = e4m3_pair(sa[gr]);
+            sb[gr] = e4m3_pair(sb[gr]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int gr = 0; gr < kChunkGroups; ++gr) {
+                const uint32_t wa = k == 0 ? ka[gr].x : k == 1 ? ka[gr].y : k == 2 ? ka[gr].z : ka[gr].w;
+                const uint32_t wb = k == 0 ? kb[gr].x : k == 1 ? kb[gr].y : k == 2 ? kb[gr].z : kb[gr].w;
+                const uint32_t fa = __byte_perm(sa[gr], sa[gr], k < 2 ? 0x1010 : 0x3232);
+                const uint32_t fb = __byte_perm(sb[gr], sb[gr], k < 2 ? 0x1010 : 0x3232);
+                uint32_t u[8] = {e2m1_pair<0>(wa), e2m1_pair<0>(wb), e2m1_pair<1>(wa), e2m1_pair<1>(wb),
+                                 e2m1_pair<2>(wa), e2m1_pair<2>(wb), e2m1_pair<3>(wa), e2m1_pair<3>(wb)};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = FP16::mul2(u[i], i & 1 ? fb : fa);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma(x[gr][nt], u[0], u[1], u[2], u[3], qf[nt][4 * k], qf[nt][4 * k + 1]);
+                    mma(x[gr][nt], u[4], u[5], u[6], u[7], qf[nt][4 * k + 2], qf[nt][4 * k + 3]);
+                }
+            }
+        }
+
+        // ---- probabilities 2^(x - m)
+        uint32_t hidden = 0;  // bit (gr, nt, e): the key is not seen by the column
+        if (!full) {
+#pragma unroll
+            for (int gr = 0; gr < kChunkGroups; ++gr)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int t = tok0 + gr * 16 + tok_of_row(g) + (e >> 1) * 8;
+                        const int col = nt * 8 + 2 * c + (e & 1);
+                        const int pos = s.first_pos + query_of(p, s, col0 + col);
+                        const bool seen = (here >> gr & 1u) && col < cols && t <= pos &&
+                                          (p.window == 0 || t > pos - p.window);
+                        hidden |= (uint32_t)!seen << ((gr * NT + nt) * 4 + e);
+                    }
+        }
+        float y[kChunkGroups][NT][4], sum[NT][2];
+        bool high = false;
+        auto exps = [&](int nt) {
+#pragma unroll
+            for (int gr = 0; gr < kChunkGroups; ++gr)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    y[gr][nt][e] = fmaf(x[gr][nt][e], cs[nt][e & 1], -m[nt][e & 1]);
+            if (!full) {
+#pragma unroll
+                for (int gr = 0; gr < kChunkGroups; ++gr)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (hidden & (1u << ((gr * NT + nt) * 4 + e))) y[gr][nt][e] = -INFINITY;
+            }
+            sum[nt][0] = sum[nt][1] = 0.0f;
+#pragma unroll
+            for (int gr = 0; gr < kChunkGroups; ++gr)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    y[gr][nt][e] = ex2(y[gr][nt][e]);
+                    sum[nt][e & 1] += y[gr][nt][e];
+                }
+            high |= sum[nt][0] > kPMax || sum[nt][1] > kPMax;
+        };
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) exps(nt);
+        if (__any_sync(0xFFFFFFFFu, high)) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float top = kNoMax;
+#pragma unroll
+                    for (int gr = 0; gr < kChunkGroups; ++gr)
+#pragma unroll
+                        for (int e = k; e < 4; e += 2)
+                            if (!(hidden & (1u << ((gr * NT + nt) * 4 + e))))
+                                top = fmaxf(top, x[gr][nt][e] * cs[nt][k]);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                    const float now = fmaxf(m[nt][k], top);
+                    const float f = ex2(m[nt][k] - now);
+                    m[nt][k] = now;
+                    l[nt][k] *= f;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        o[nt][j][k] *= f;
+                        o[nt][j][k + 2] *= f;
+                    }
+                }
+                exps(nt);
+            }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            l[nt][0] += sum[nt][0];
+            l[nt][1] += sum[nt][1];
+        }
+        uint32_t pf[kChunkGroups][NT][2];
+#pragma unroll
+        for (int gr = 0; gr < kChunkGroups; ++gr)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                pf[gr][nt][0] = transpose8x8(FP16::pack(y[gr][nt][0], y[gr][nt][1]));
+                pf[gr][nt][1] = transpose8x8(FP16::pack(y[gr][nt][2], y[gr][nt][3]));
+            }
+
+        // ---- O^T += V^T P^T
+#pragma unroll
+        for (int gr = 0; gr < kChunkGroups; ++gr) {
+            const uint32_t base = stage + gr * kKVGroupBytes;
+            const uint2 v0 = lds8_at<0>(base + w.vread), v1 = lds8_at<256>(base + w.vread);
+            const uint2 v2 = lds8_at<512>(base + w.vread), v3 = lds8_at<768>(base + w.vread);
+            uint32_t f01 = lds1_at<0>(base + w.vsread) | (lds1_at<32>(base + w.vsread) << 8);
+            uint32_t f23 = lds1_at<64>(base + w.vsread) | (lds1_at<96>(base + w.vsread) << 8);
+            if (!full) {  // bytes of keys that nobody sees may be anything
+                const int t = tok0 + gr * 16 + c;
+                const int end = here >> gr & 1u ? blk_hi : 0;
+                if (t >= end) f01 &= 0xFF00u;
+                if (t + 4 >= end) f01 &= 0x00FFu;
+                if (t + 8 >= end) f23 &= 0xFF00u;
+                if (t + 12 >= end) f23 &= 0x00FFu;
+            }
+            const uint32_t sa = e4m3_pair(f01), sb = e4m3_pair(f23);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t w0 = k ? v0.y : v0.x, w1 = k ? v1.y : v1.x;
+                const uint32_t w2 = k ? v2.y : v2.x, w3 = k ? v3.y : v3.x;
+                const uint32_t lo = 0x0F0F0F0Fu;
+                const uint32_t ea = (w0 & lo) | ((w1 << 4) & ~lo), oa = ((w0 >> 4) & lo) | (w1 & ~lo);
+                const uint32_t eb = (w2 & lo) | ((w3 << 4) & ~lo), ob = ((w2 >> 4) & lo) | (w3 & ~lo);
+                uint32_t u[16] = {e2m1_pair<0>(ea), e2m1_pair<0>(oa), e2m1_pair<0>(eb), e2m1_pair<0>(ob),
+                                  e2m1_pair<1>(ea), e2m1_pair<1>(oa), e2m1_pair<1>(eb), e2m1_pair<1>(ob),
+                                  e2m1_pair<2>(ea), e2m1_pair<2>(oa), e2m1_pair<2>(eb), e2m1_pair<2>(ob),
+                                  e2m1_pair<3>(ea), e2m1_pair<3>(oa), e2m1_pair<3>(eb), e2m1_pair<3>(ob)};
+#pragma unroll
+                for (int i = 0; i < 16; ++i) u[i] = FP16::mul2(u[i], i & 2 ? sb : sa);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma(o[nt][4 * k + i], u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3], pf[gr][nt][0],
+                            pf[gr][nt][1]);
+            }
+        }
+        stage = stage == (kStages - 1) * kChunkBytes ? 0 : stage + kChunkBytes;
+        filled = filled == (kStages - 1) * kChunkBytes ? 0 : filled + kChunkBytes;
+    }
+
+    // ---- join the warps: O of column k in the warp's ring, 512 bytes each
+    cp_async_wait<0>();
+    __syncwarp();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float sum = l[nt][k];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
+            const int col = nt * 8 + 2 * c + k;
+            if (g == 0) stats[col] = make_float2(m[nt][k], sum);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<float2 *>(w.o + col * 128 + 16 * g + 2 * j) =
+                    make_float2(o[nt][j][k], o[nt][j][k + 2]);
+        }
+}
+
 template <typename DT, int NT>
 __global__ void __launch_bounds__(kThreads, (NT == 1 ? 16 : 8) / kWarps)
 paged_attn_split_kernel(const PagedAttnParams p)
 {
-    static_assert(kStages * kChunkBytes >= 8 * NT * 128 * 4, "a warp's ring holds its part of O at the end");
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int64_t scan[kWarps];
     __shared__ int start_seq;
@@ -195,7 +567,6 @@ paged_attn_split_kernel(const PagedAttnParams p)
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int g = lane >> 2, c = lane & 3;
     PartInfo *info = reinterpret_cast<PartInfo *>(p.workspace) + 2 * blockIdx.x;
     float *parts = reinterpret_cast<float *>(p.workspace + kInfoBytes) +
                    (int64_t)blockIdx.x * 2 * kPartFloats<NT>;
@@ -243,17 +614,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
     int b = start_seq;
     int64_t rem = start_rem;
 
-    const uint32_t ring = smem_addr(smem) + warp * (kStages * kChunkBytes);
-    float *warp_o = reinterpret_cast<float *>(smem + warp * (kStages * kChunkBytes));
-    // where the lane's 16-byte pieces of a group go (the fifth: lanes 0-15)
-    const uint32_t kdst = ring + row_of_tok(lane >> 2) * 64 + (lane & 3) * 16;  // + 512: tokens 8-15
-    const uint32_t vdst = ring + kKVCodesV + (lane >> 2) * 64 + (((lane & 3) ^ ((lane >> 3) & 1) * 2) * 16);
-    const uint32_t fdst = ring + kKVScalesK + lane * 16;
-    // where it reads them
-    const uint32_t kread = ring + g * 64 + c * 16;
-    const uint32_t vread = ring + kKVCodesV + c * 64 + (((g >> 1) ^ ((c >> 1) & 1) * 2) * 16) + (g & 1) * 8;
-    const uint32_t ksread = ring + kKVScalesK + tok_of_row(g) * 8 + 2 * c;
-    const uint32_t vsread = ring + kKVScalesV + c * 8 + g;
+    const WarpRing ring(smem + warp * (kStages * kChunkBytes));
     const float inv_kgs = 1.0f / ld_f32(p.k_gs);
 
     Seq s = load_seq(p, b);
@@ -275,327 +636,9 @@ paged_attn_split_kernel(const PagedAttnParams p)
         if (ntile <= 0) continue;  // no more than the item's overhead
         const int head = item / ct.blocks, block = item - head * ct.blocks;
         const int col0 = block * 8 * NT, cols = min(8 * NT, s.nq * p.per - col0);
-        // keys that the block's columns see: all of [need_lo, need_hi) by every
-        // one, nothing from blk_hi on by any
-        const int i_first = query_of(p, s, col0), i_last = query_of(p, s, col0 + cols - 1);
-        const int blk_hi = s.first_pos + i_last + 1;
-        const int need_hi = s.first_pos + i_first + 1;
-        const int need_lo = p.window > 0 ? blk_hi - p.window : 0;
         const int t0 = s.lo + tile0 * kChunk;
-        const int t1 = min(blk_hi, t0 + ntile * kChunk);  // may lie before t0: nothing to do
-        const int chunks = t1 > t0 + warp * kChunk
-                               ? (t1 - t0 - warp * kChunk + kWarps * kChunk - 1) / (kWarps * kChunk)
-                               : 0;  // of this warp
-
-        // ---- queries' loads: columns nt * 8 + g (past the last: the first
-        // again; a load under a condition would be waited for at once),
-        // channels 32 c .. + 31
-        uint4 qv[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int col = col0 + (nt * 8 + g < cols ? nt * 8 + g : 0);
-            const int i = query_of(p, s, col), h = head * p.per + col - i * p.per;
-            const uint8_t *src =
-                static_cast<const uint8_t *>(p.q) + ((s.q0 + i) * p.q_stride + (int64_t)h * 128 + 32 * c) * 2;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) qv[nt][k] = ld_keep16(src + 16 * k);
-        }
-
-        // ---- groups of the warp's chunks, 32 groups at a time: lane kChunkGroups
-        // i + j holds where group j of chunk i lies in the cache (-1: nowhere)
-        auto token_of = [&](int batch) {
-            return t0 + (warp + kWarps * (batch * kBatch + lane / kChunkGroups)) * kChunk + lane % kChunkGroups * 16;
-        };
-        // the page id of the batch's token, or of the part's first token where
-        // it has none; and the place, once the id is there
-        auto find = [&](int batch) {
-            const int token = token_of(batch);
-            return ld_s32(p.table + (int64_t)b * p.table_stride + ((token < t1 ? token : t0) >> 4) / p.groups);
-        };
-        auto place = [&](int batch, int id) {
-            const int token = token_of(batch), slot = token >> 4;
-            return token < t1 && id >= 0 && id < p.num_pages
-                       ? (int)(((int64_t)id * p.hk + head) * p.groups + slot % p.groups)
-                       : -1;
-        };
-        auto fetch = [&](int i, int from, uint32_t stage) {  // starts the copies of chunk i
-#pragma unroll
-            for (int gr = 0; gr < kChunkGroups; ++gr) {
-                const int at = __shfl_sync(0xFFFFFFFFu, from, i % kBatch * kChunkGroups + gr);
-                if (at >= 0 && i < chunks) {
-                    const uint8_t *src = p.pool + (int64_t)at * kKVGroupBytes + lane * 16;
-                    const uint32_t d = stage + gr * kKVGroupBytes;
-                    cp16_at<0, 0>(d + kdst, src);
-                    cp16_at<512, 512>(d + kdst, src);
-                    cp16_at<0, 1024>(d + vdst, src);
-                    cp16_at<512, 1536>(d + vdst, src);
-                    if (lane < 16) cp16_at<0, 2048>(d + fdst, src);
-                }
-            }
-            cp_async_commit();
-        };
-        int near_id = -1, far_id = -1;
-        if (t1 > t0) {
-            near_id = find(0);
-            far_id = find(1);
-        }
-        int near = place(0, near_id);
-        for (int i = 0; i < kStages - 1; ++i) fetch(i, near, i * kChunkBytes);
-        uint32_t near_ok = __ballot_sync(0xFFFFFFFFu, near >= 0);
-        int far = -1;  // from the chunk on whose fetch needs it
-        uint32_t stage = 0, filled = (kStages - 1) * kChunkBytes;  // of chunk it, of the next to fetch
-
-        // ---- queries as the B operand; each row by a power of two so that fp16
-        // holds it
-        uint32_t qf[NT][16];
-        float cs[NT][2], m[NT][2], l[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            uint4 (&v)[4] = qv[nt];
-            float f = 1.0f, back = 1.0f;
-            if (std::is_same<DT, BF16>::value) {
-                float a = 0.0f;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float e[8];
-                    unpack8<DT>(v[k], e);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) a = fmaxf(a, fabsf(e[j]));
-                }
-                a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 1));
-                a = fmaxf(a, __shfl_xor_sync(0xFFFFFFFFu, a, 2));
-                const float2 pw = row_power(a);
-                f = pw.x;
-                back = pw.y;
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if (std::is_same<DT, BF16>::value) {
-                    float e[8];
-                    unpack8<DT>(v[k], e);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) e[j] *= f;
-                    v[k] = pack8<FP16>(e);
-                }
-                qf[nt][4 * k] = v[k].x;
-                qf[nt][4 * k + 1] = v[k].y;
-                qf[nt][4 * k + 2] = v[k].z;
-                qf[nt][4 * k + 3] = v[k].w;
-            }
-            const float scale = fmaxf(p.scale * inv_kgs * back, kLeastScale);
-            cs[nt][0] = __shfl_sync(0xFFFFFFFFu, scale, 8 * c);
-            cs[nt][1] = __shfl_sync(0xFFFFFFFFu, scale, 8 * c + 4);
-            m[nt][0] = m[nt][1] = kNoMax;
-            l[nt][0] = l[nt][1] = 0.0f;
-        }
-        float o[NT][8][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[nt][j][e] = 0.0f;
-
-        for (int it = 0; it < chunks; ++it) {
-            cp_async_wait<kStages - 2>();
-            __syncwarp();  // everyone's copies have landed; everyone is done with the stage before
-            if (it > 0 && it % kBatch == 0) {
-                near = far;
-                far_id = find(it / kBatch + 1);
-                near_ok = __ballot_sync(0xFFFFFFFFu, near >= 0);
-            }
-            if (it % kBatch == kBatch - kStages + 1) far = place(it / kBatch + 1, far_id);
-            fetch(it + kStages - 1, it % kBatch + kStages - 1 < kBatch ? near : far, filled);
-            const int tok0 = t0 + (warp + kWarps * it) * kChunk;
-            const uint32_t here = near_ok >> (it % kBatch * kChunkGroups);  // bit gr: the group is readable
-            const bool full = tok0 >= need_lo && tok0 + kChunk <= need_hi && (here & kAll) == kAll;
-
-            // ---- S^T = K Q^T, the two groups' chains of products side by side
-            float x[kChunkGroups][NT][4];
-            uint4 ka[kChunkGroups], kb[kChunkGroups];
-            uint32_t sa[kChunkGroups], sb[kChunkGroups];
-#pragma unroll
-            for (int gr = 0; gr < kChunkGroups; ++gr) {
-                const uint32_t base = stage + gr * kKVGroupBytes;
-                ka[gr] = lds16_at<0>(base + kread);
-                kb[gr] = lds16_at<512>(base + kread);
-                sa[gr] = lds2_at<0>(base + ksread);
-                sb[gr] = lds2_at<64>(base + ksread);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[gr][nt][e] = 0.0f;
-            }
-#pragma unroll
-            for (int gr = 0; gr < kChunkGroups; ++gr) {
-                sa[gr] = e4m3_pair(sa[gr]);
-                sb[gr] = e4m3_pair(sb[gr]);
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-#pragma unroll
-                for (int gr = 0; gr < kChunkGroups; ++gr) {
-                    const uint32_t wa = k == 0 ? ka[gr].x : k == 1 ? ka[gr].y : k == 2 ? ka[gr].z : ka[gr].w;
-                    const uint32_t wb = k == 0 ? kb[gr].x : k == 1 ? kb[gr].y : k == 2 ? kb[gr].z : kb[gr].w;
-                    const uint32_t fa = __byte_perm(sa[gr], sa[gr], k < 2 ? 0x1010 : 0x3232);
-                    const uint32_t fb = __byte_perm(sb[gr], sb[gr], k < 2 ? 0x1010 : 0x3232);
-                    uint32_t u[8] = {e2m1_pair<0>(wa), e2m1_pair<0>(wb), e2m1_pair<1>(wa), e2m1_pair<1>(wb),
-                                     e2m1_pair<2>(wa), e2m1_pair<2>(wb), e2m1_pair<3>(wa), e2m1_pair<3>(wb)};
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) u[i] = FP16::mul2(u[i], i & 1 ? fb : fa);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma(x[gr][nt], u[0], u[1], u[2], u[3], qf[nt][4 * k], qf[nt][4 * k + 1]);
-                        mma(x[gr][nt], u[4], u[5], u[6], u[7], qf[nt][4 * k + 2], qf[nt][4 * k + 3]);
-                    }
-                }
-            }
-
-            // ---- probabilities 2^(x - m)
-            uint32_t hidden = 0;  // bit (gr, nt, e): the key is not seen by the column
-            if (!full) {
-#pragma unroll
-                for (int gr = 0; gr < kChunkGroups; ++gr)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int t = tok0 + gr * 16 + tok_of_row(g) + (e >> 1) * 8;
-                            const int col = nt * 8 + 2 * c + (e & 1);
-                            const int pos = s.first_pos + query_of(p, s, col0 + col);
-                            const bool seen = (here >> gr & 1u) && col < cols && t <= pos &&
-                                              (p.window == 0 || t > pos - p.window);
-                            hidden |= (uint32_t)!seen << ((gr * NT + nt) * 4 + e);
-                        }
-            }
-            float y[kChunkGroups][NT][4], sum[NT][2];
-            bool high = false;
-            auto exps = [&](int nt) {
-#pragma unroll
-                for (int gr = 0; gr < kChunkGroups; ++gr)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        y[gr][nt][e] = fmaf(x[gr][nt][e], cs[nt][e & 1], -m[nt][e & 1]);
-                if (!full) {
-#pragma unroll
-                    for (int gr = 0; gr < kChunkGroups; ++gr)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (hidden & (1u << ((gr * NT + nt) * 4 + e))) y[gr][nt][e] = -INFINITY;
-                }
-                sum[nt][0] = sum[nt][1] = 0.0f;
-#pragma unroll
-                for (int gr = 0; gr < kChunkGroups; ++gr)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        y[gr][nt][e] = ex2(y[gr][nt][e]);
-                        sum[nt][e & 1] += y[gr][nt][e];
-                    }
-                high |= sum[nt][0] > kPMax || sum[nt][1] > kPMax;
-            };
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) exps(nt);
-            if (__any_sync(0xFFFFFFFFu, high)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        float top = kNoMax;
-#pragma unroll
-                        for (int gr = 0; gr < kChunkGroups; ++gr)
-#pragma unroll
-                            for (int e = k; e < 4; e += 2)
-                                if (!(hidden & (1u << ((gr * NT + nt) * 4 + e))))
-                                    top = fmaxf(top, x[gr][nt][e] * cs[nt][k]);
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                        const float now = fmaxf(m[nt][k], top);
-                        const float f = ex2(m[nt][k] - now);
-                        m[nt][k] = now;
-                        l[nt][k] *= f;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            o[nt][j][k] *= f;
-                            o[nt][j][k + 2] *= f;
-                        }
-                    }
-                    exps(nt);
-                }
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                l[nt][0] += sum[nt][0];
-                l[nt][1] += sum[nt][1];
-            }
-            uint32_t pf[kChunkGroups][NT][2];
-#pragma unroll
-            for (int gr = 0; gr < kChunkGroups; ++gr)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    pf[gr][nt][0] = transpose8x8(FP16::pack(y[gr][nt][0], y[gr][nt][1]));
-                    pf[gr][nt][1] = transpose8x8(FP16::pack(y[gr][nt][2], y[gr][nt][3]));
-                }
-
-            // ---- O^T += V^T P^T
-#pragma unroll
-            for (int gr = 0; gr < kChunkGroups; ++gr) {
-                const uint32_t base = stage + gr * kKVGroupBytes;
-                const uint2 v0 = lds8_at<0>(base + vread), v1 = lds8_at<256>(base + vread);
-                const uint2 v2 = lds8_at<512>(base + vread), v3 = lds8_at<768>(base + vread);
-                uint32_t f01 = lds1_at<0>(base + vsread) | (lds1_at<32>(base + vsread) << 8);
-                uint32_t f23 = lds1_at<64>(base + vsread) | (lds1_at<96>(base + vsread) << 8);
-                if (!full) {  // bytes of keys that nobody sees may be anything
-                    const int t = tok0 + gr * 16 + c;
-                    const int end = here >> gr & 1u ? blk_hi : 0;
-                    if (t >= end) f01 &= 0xFF00u;
-                    if (t + 4 >= end) f01 &= 0x00FFu;
-                    if (t + 8 >= end) f23 &= 0xFF00u;
-                    if (t + 12 >= end) f23 &= 0x00FFu;
-                }
-                const uint32_t sa = e4m3_pair(f01), sb = e4m3_pair(f23);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint32_t w0 = k ? v0.y : v0.x, w1 = k ? v1.y : v1.x;
-                    const uint32_t w2 = k ? v2.y : v2.x, w3 = k ? v3.y : v3.x;
-                    const uint32_t lo = 0x0F0F0F0Fu;
-                    const uint32_t ea = (w0 & lo) | ((w1 << 4) & ~lo), oa = ((w0 >> 4) & lo) | (w1 & ~lo);
-                    const uint32_t eb = (w2 & lo) | ((w3 << 4) & ~lo), ob = ((w2 >> 4) & lo) | (w3 & ~lo);
-                    uint32_t u[16] = {e2m1_pair<0>(ea), e2m1_pair<0>(oa), e2m1_pair<0>(eb), e2m1_pair<0>(ob),
-                                      e2m1_pair<1>(ea), e2m1_pair<1>(oa), e2m1_pair<1>(eb), e2m1_pair<1>(ob),
-                                      e2m1_pair<2>(ea), e2m1_pair<2>(oa), e2m1_pair<2>(eb), e2m1_pair<2>(ob),
-                                      e2m1_pair<3>(ea), e2m1_pair<3>(oa), e2m1_pair<3>(eb), e2m1_pair<3>(ob)};
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) u[i] = FP16::mul2(u[i], i & 2 ? sb : sa);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
-                            mma(o[nt][4 * k + i], u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3], pf[gr][nt][0],
-                                pf[gr][nt][1]);
-                }
-            }
-            stage = stage == (kStages - 1) * kChunkBytes ? 0 : stage + kChunkBytes;
-            filled = filled == (kStages - 1) * kChunkBytes ? 0 : filled + kChunkBytes;
-        }
-
         const float v_gs = ld_f32(p.v_gs);
-        // ---- join the warps: O of column k in the warp's ring, 512 bytes each
-        cp_async_wait<0>();
-        __syncwarp();
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                float sum = l[nt][k];
-#pragma unroll
-                for (int d = 4; d < 32; d <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, d);
-                const int col = nt * 8 + 2 * c + k;
-                if (g == 0) stats[warp][col] = make_float2(m[nt][k], sum);
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<float2 *>(warp_o + col * 128 + 16 * g + 2 * j) =
-                        make_float2(o[nt][j][k], o[nt][j][k + 2]);
-            }
+        attend<DT, NT>(p, s, b, head, col0, cols, t0, t0 + ntile * kChunk, warp, kWarps, inv_kgs, ring, stats[warp]);
         __syncthreads();
         constexpr int kPerCol = kThreads / (8 * NT), kVals = 128 / kPerCol;
         const int col = threadIdx.x / kPerCol, d0 = (threadIdx.x % kPerCol) * kVals;
@@ -627,6 +670,59 @@ paged_attn_split_kernel(const PagedAttnParams p)
         if (threadIdx.x == 0 && ntile != ct.tiles)
             info[tile0 == 0] = PartInfo{1, tile0 + ntile == ct.tiles, b, head, block};
         __syncthreads();
+    }
+}
+
+// The same for calls that are short: a cluster of kCluster CTAs takes an item, its
+// warps the item's chunks in turn, and the parts join through the cluster's
+// shared memory, in one launch.
+template <typename DT, int NT>
+__global__ void __launch_bounds__(kThreads, (NT == 1 ? 16 : 8) / kWarps)
+paged_attn_cluster_kernel(const PagedAttnParams p)
+{
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float2 stats[kWarps][8 * NT];
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, rank = blockIdx.x % kCluster;
+    const int pair = blockIdx.x / kCluster, b = pair / p.hk, head = pair - b * p.hk;
+    const Seq s = load_seq(p, b);
+    const float inv_kgs = 1.0f / ld_f32(p.k_gs), v_gs = ld_f32(p.v_gs);
+    const WarpRing ring(smem + warp * (kStages * kChunkBytes));
+    const int columns = s.nq * p.per;
+    for (int col0 = 0; col0 < columns; col0 += 8 * NT) {
+        const int cols = min(8 * NT, columns - col0);
+        attend<DT, NT>(p, s, b, head, col0, cols, s.lo, s.hi, rank * kWarps + warp, kCluster * kWarps, inv_kgs, ring,
+                       stats[warp]);
+        cluster_sync();
+        // column rank (and rank + 8): a thread a channel over all warps' parts
+        for (int col = rank; col < cols; col += kCluster) {
+            float m[kParts], l[kParts], o[kParts], top = kNoMax, sum = 0.0f, v = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+                const uint32_t at = cluster_addr(&stats[i % kWarps][col], i / kWarps);
+                m[i] = ld_cluster(at);
+                l[i] = ld_cluster(at + 4);
+            }
+#pragma unroll
+            for (int i = 0; i < kParts; ++i)
+                o[i] = ld_cluster(cluster_addr(smem + i % kWarps * (kStages * kChunkBytes), i / kWarps) +
+                                  (col * 128 + threadIdx.x) * 4);
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) top = fmaxf(top, m[i]);
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) {
+                const float f = ex2(m[i] - top);
+                sum = fmaf(f, l[i], sum);
+                v = fmaf(f, o[i], v);
+            }
+            const int at = col0 + col, i = query_of(p, s, at);
+            const int64_t row = (int64_t)(s.q0 + i) * p.hq + head * p.per + at - i * p.per;
+            const float x = v * out_factor(sum, v_gs);
+            static_cast<uint16_t *>(p.out)[row * 128 + threadIdx.x] = (uint16_t)DT::pack(x, 0.0f);
+            if (p.lse != nullptr && threadIdx.x == 0) p.lse[row] = lse_of(top, sum);
+        }
+        cluster_sync();  // the parts have been read
     }
 }
 
@@ -710,6 +806,33 @@ cudaError_t launch_split(const PagedAttnParams &p, int dev, cudaStream_t stream)
     return launch_pdl(paged_attn_join_kernel<DT, NT>, grid, 256, 0, stream, p, grid);
 }
 
+template <typename DT, int NT>
+cudaError_t launch_cluster(const PagedAttnParams &p, int dev, cudaStream_t stream)
+{
+    static_assert(kThreads == 128, "the join takes a thread a channel");
+    static std::atomic<int> ready[64];
+    auto kern = paged_attn_cluster_kernel<DT, NT>;
+    if (dev >= 64 || !ready[dev].load(std::memory_order_relaxed)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready[dev].store(1, std::memory_order_relaxed);
+    }
+    return launch_pdl_cluster(kern, (unsigned)(p.n_seqs * p.hk), kCluster, kThreads, kSmem, stream, p);
+}
+
+// Whether the cluster form is taken: all its CTAs run at once, and the sequences
+// are not so long that cutting them finer pays.  Measured against the split
+// form, 8 KV heads of 2 queries: 1 sequence of 100, 1000, 4000, 16,000 and 32,000
+// keys 5.3, 5.3, 7.8, 18.2 and 31.7 us (6.9, 9.0, 11.3, 18.5 and 21.8), 9 of them
+// 8.7, 9.0, 13.4, 36 and 65 (7.2, 12.6, 19.0, 45 and 74); 2 KV heads of 16
+// queries, 9 sequences 10.2, 11.0, 13.8, 28.5 and 48 (8.7, 14.7, 18.9, 26.8 and
+// 37), 18 sequences of 1000 and 4000 keys 16.6 and 22.0 (15.9 and 20.9).
+template <int NT>
+bool is_short(const PagedAttnParams &p, int dev)
+{
+    return (int64_t)p.n_seqs * p.hk * kCluster <= (NT == 1 ? 4 : 1) * device_sms(dev) && p.max_keys <= 16384;
+}
+
 }  // namespace
 
 size_t paged_attn_workspace_bytes(int, int)
@@ -728,7 +851,8 @@ cudaError_t launch_paged_attn(const PagedAttnParams &p, cudaStream_t stream)
     const int64_t cols = (int64_t)p.per * p.max_q;
     PagedAttnParams few = p;
     few.few = INT_MAX;
-    if (cols <= 8) return launch_split<DT, 1>(few, dev, stream);
+    if (cols <= 8)
+        return is_short<1>(few, dev) ? launch_cluster<DT, 1>(few, dev, stream) : launch_split<DT, 1>(few, dev, stream);
     // This kernel's time goes with blocks of 16 columns, spread over every SM;
     // the tensor-memory kernel's with waves of 256-row blocks, each on one SM for
     // all its keys.  Measured at 8 KV heads, 16-column blocks here against
@@ -739,7 +863,8 @@ cudaError_t launch_paged_attn(const PagedAttnParams &p, cudaStream_t stream)
     const int64_t rows = (int64_t)p.per * p.n_tokens, sms = device_sms(dev);
     const int64_t blocks16 = (rows / 16 + p.n_seqs) * p.hk, blocks256 = (rows / 256 + p.n_seqs) * p.hk;
     if (p.q_starts == nullptr || cols <= kFewColumns || blocks16 <= 270 * ((blocks256 + sms - 1) / sms))
-        return launch_split<DT, 2>(few, dev, stream);
+        return cols <= 16 && is_short<2>(few, dev) ? launch_cluster<DT, 2>(few, dev, stream)
+                                                : launch_split<DT, 2>(few, dev, stream);
     few.few = kFewColumns;
     e = launch_split<DT, 2>(few, dev, stream);
     return e != cudaSuccess ? e : launch_paged_attn_tc<DT>(few, stream);

@@ -162,6 +162,22 @@ def test_decode(hq, hk, page, dt):
     run_decode(Cache(1, LENS, hk, page), hq, dt, seed=hq)
 
 
+@pytest.mark.parametrize("hq, hk, page, dt", [(2, 2, 48, "fp16"), (16, 2, 16, "bf16"), (32, 2, 32, "bf16"),
+                                              (20, 1, 64, "fp16")])
+def test_decode_wide_table(hq, hk, page, dt):
+    """Tables wider than the sequences need (long-context capacity)."""
+    c = Cache(30, LENS, hk, page, stride_extra=20000 // page)
+    run_decode(c, hq, dt)
+    run_extend(c, hq, [1, 0, 2, 1, 3, 1, 1, 2, 1, 1, 2, 4], dt, window=40)
+
+
+@pytest.mark.parametrize("seqs, hq, hk", [(9, 16, 8), (72, 8, 1), (9, 32, 2), (300, 4, 4)])
+def test_decode_batches(seqs, hq, hk):
+    lens = np.random.default_rng(seqs).integers(0, 600, seqs)
+    lens[seqs // 2] = 2100
+    run_decode(Cache(31, lens.tolist(), hk, 32), hq, "bf16")
+
+
 @pytest.mark.parametrize("window", [1, 5, 16, 100, 511, 5000])
 def test_decode_window(window):
     run_decode(Cache(2, LENS, 2, 32), 8, "bf16", window=window)
