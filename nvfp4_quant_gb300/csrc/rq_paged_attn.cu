@@ -820,13 +820,19 @@ cudaError_t launch_cluster(const PagedAttnParams &p, int dev, cudaStream_t strea
     return launch_pdl_cluster(kern, (unsigned)(p.n_seqs * p.hk), kCluster, kThreads, kSmem, stream, p);
 }
 
-// Whether the cluster form is taken: all its CTAs run at once, and the sequences
-// are not so long that cutting them finer pays.  Measured against the split
-// form, 8 KV heads of 2 queries: 1 sequence of 100, 1000, 4000, 16,000 and 32,000
-// keys 5.3, 5.3, 7.8, 18.2 and 31.7 us (6.9, 9.0, 11.3, 18.5 and 21.8), 9 of them
-// 8.7, 9.0, 13.4, 36 and 65 (7.2, 12.6, 19.0, 45 and 74); 2 KV heads of 16
-// queries, 9 sequences 10.2, 11.0, 13.8, 28.5 and 48 (8.7, 14.7, 18.9, 26.8 and
-// 37), 18 sequences of 1000 and 4000 keys 16.6 and 22.0 (15.9 and 20.9).
+// Whether the cluster form is taken: all its CTAs run at once, and the table has
+// no room for sequences so long that cutting them finer pays.  Measured, with the
+// split form in brackets.  8 KV heads of 2 queries: 1 sequence of 100, 1000, 4000,
+// 16,000 and 32,000 keys 5.3, 5.3, 7.8, 18.2 and 31.7 us (6.9, 9.0, 11.3, 18.5
+// and 21.8), 4 of 1000, 8000 and 16,000 7.7, 18.8 and 31.8 (10.5, 18.3 and 24.6),
+// 9 of 100, 1000, 4000 and 16,000 8.7, 9.0, 13.4 and 36 (7.2, 12.6, 19.0 and 45).
+// 1 KV head of 8, 72 sequences of 100, 1000 and 16,000 12.4, 13.6 and 39 (7.3,
+// 14.1 and 47).  2 KV heads of 16: 9 sequences of 100, 1000, 4000 and 16,000 10.2,
+// 11.0, 13.8 and 28.5 (8.7, 14.7, 18.9 and 26.8), 18 of 1000 and 4000 16.6 and
+// 22.0 (15.9 and 20.9).  So to 8000 keys it wins but for the very short ones; at
+// 16,000 it is 0.8 to 1.5 times as fast, and the limit is a table's room, that
+// most sequences do not fill.  The lengths are on the device: the host cannot
+// choose by them.
 template <int NT>
 bool is_short(const PagedAttnParams &p, int dev)
 {
