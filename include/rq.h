@@ -457,9 +457,10 @@ rq_status rq_qkv_rope_nvfp4_kv_append(
  *                   last page are not read.
  *   kv_lens         [n_seqs] int32 keys of each sequence, the new tokens among
  *                   them; clamped to [0, pages_per_seq * page_size].  Cache
- *                   bytes of later tokens may hold anything; scale bytes of
- *                   the tokens themselves are finite E4M3 values (the append
- *                   writes no others).
+ *                   bytes of tokens that no query of the sequence sees (later
+ *                   ones, ones before the window) may hold anything; scale
+ *                   bytes of the others are finite E4M3 values (the append
+ *                   writes no others for finite k and v).
  *   out             [n_tokens, n_q_heads, head_dim] dt
  *   lse             [n_tokens, n_q_heads] fp32, or NULL
  *   workspace       rq_paged_attn_nvfp4_workspace_bytes() bytes, 16-byte
@@ -467,7 +468,7 @@ rq_status rq_qkv_rope_nvfp4_kv_append(
  *                   use until the call's work on the stream is done: calls (or
  *                   captured graphs) that may run at the same time need one
  *                   each.  A smaller one returns RQ_ERR_SHAPE.
- *   sm_scale > 0; window >= 0 (0: none); pages_per_seq * page_size <=
+ *   sm_scale > 0, finite (also times log2 e); window >= 0 (0: none); pages_per_seq * page_size <=
  *   RQ_ATTN_MAX_KEYS, n_tokens <= RQ_ATTN_MAX_TOKENS, n_tokens * n_q_heads <
  *   2^31, n_seqs <= RQ_ATTN_MAX_SEQS.
  *

@@ -549,6 +549,8 @@ def _paged_attn(q, kv_pool, page_size, block_table, q_starts, max_q_len, kv_lens
         raise ValueError("block_table's rows must be contiguous")
     if n < 2:
         row = per
+    if workspace is None or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor")
     tail = (_typed(kv_lens, _I32, n, "kv_lens"), sm_scale, window, _typed(k_gs, _F32, 1, "k_global_scale"),
             _typed(v_gs, _F32, 1, "v_global_scale"), _typed(out, q.dtype, t * hq * d, "out"),
             None if lse is None else _typed(lse, _F32, t * hq, "lse"), workspace.data_ptr(),
@@ -704,6 +706,8 @@ def qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos_si
 
 
 def _attn_buffers(q, kv_pool, with_lse, workspace, stream):
+    if q.dim() != 3 or kv_pool.dim() != 3:
+        raise ValueError("q and kv_pool must have three dimensions")
     if stream is not None:
         with _on_stream(stream, q.device):
             return _attn_buffers(q, kv_pool, with_lse, workspace, None)

@@ -5,6 +5,7 @@
 #include "rq_launch.h"
 
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 
@@ -505,6 +506,8 @@ int64_t pool_bytes(int64_t num_pages, int page_size, int heads)
     return num_pages * heads * (page_size / 16) * rq::kKVGroupBytes;
 }
 
+constexpr float kLog2E = 1.44269504088896340736f;
+
 // Argument checks of the attention calls, then the launch.
 rq_status attn_call(const void *q, int64_t q_token_stride, int64_t n_tokens, const int32_t *q_starts,
                     int64_t n_seqs, int64_t max_q_len, int n_q_heads, int n_kv_heads, int head_dim,
@@ -517,7 +520,7 @@ rq_status attn_call(const void *q, int64_t q_token_stride, int64_t n_tokens, con
     if (dt != RQ_BF16 && dt != RQ_FP16) return RQ_ERR_DTYPE;
     if (n_tokens < 0 || n_tokens > RQ_ATTN_MAX_TOKENS || n_seqs < 0 || n_seqs > RQ_ATTN_MAX_SEQS ||
         max_q_len < 0 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads > RQ_QK_MAX_HEADS ||
-        n_q_heads % n_kv_heads != 0 || n_tokens * n_q_heads >= (int64_t)1 << 31 || window < 0 || !(sm_scale > 0.0f))
+        n_q_heads % n_kv_heads != 0 || n_tokens * n_q_heads >= (int64_t)1 << 31 || window < 0 || !(sm_scale > 0.0f) || !std::isfinite(sm_scale * kLog2E))
         return RQ_ERR_SHAPE;
     if (head_dim != RQ_QK_HEAD_DIM) return RQ_ERR_UNSUPPORTED;
     if (!valid_pool(num_pages, page_size, n_kv_heads) || pages_per_seq < 0 ||
@@ -566,8 +569,10 @@ rq_status attn_call(const void *q, int64_t q_token_stride, int64_t n_tokens, con
     p.kv_lens = kv_lens;
     p.n_seqs = (int)n_seqs;
     p.max_q = (int)(max_q_len < n_tokens ? max_q_len : n_tokens);
-    p.scale = sm_scale * 1.44269504088896340736f;
-    p.window = window;
+    p.scale = sm_scale * kLog2E;
+    // one as long as any sequence hides nothing (and differences of positions
+    // and the window stay ints)
+    p.window = window < p.max_keys ? window : 0;
     p.k_gs = d_k_gs;
     p.v_gs = d_v_gs;
     p.out = out;

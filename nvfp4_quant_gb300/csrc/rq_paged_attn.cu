@@ -504,11 +504,12 @@ __device__ __forceinline__ void attend(const PagedAttnParams &p, const Seq &s, i
             uint32_t f23 = lds1_at<64>(base + w.vsread) | (lds1_at<96>(base + w.vsread) << 8);
             if (!full) {  // bytes of keys that nobody sees may be anything
                 const int t = tok0 + gr * 16 + c;
-                const int end = here >> gr & 1u ? blk_hi : 0;
-                if (t >= end) f01 &= 0xFF00u;
-                if (t + 4 >= end) f01 &= 0x00FFu;
-                if (t + 8 >= end) f23 &= 0xFF00u;
-                if (t + 12 >= end) f23 &= 0x00FFu;
+                const int blk_lo = p.window > 0 ? max(0, need_hi - p.window) : 0;
+                const uint32_t n = here >> gr & 1u ? blk_hi - blk_lo : 0, at = t - blk_lo;
+                if (at >= n) f01 &= 0xFF00u;
+                if (at + 4 >= n) f01 &= 0x00FFu;
+                if (at + 8 >= n) f23 &= 0xFF00u;
+                if (at + 12 >= n) f23 &= 0x00FFu;
             }
             const uint32_t sa = e4m3_pair(f01), sb = e4m3_pair(f23);
 #pragma unroll

@@ -237,7 +237,7 @@ __device__ __forceinline__ void decode_row(const Row &r, uint32_t to)
 // A producer thread's token of each tile: where it lies, from tile to tile
 // without a division, and the page id of one tile further ahead.
 struct Feed {
-    int tok, hi, at, page, in, pages, rest, id;
+    int tok, first, hi, at, page, in, pages, rest, id;
     const int32_t *table;
     const uint8_t *pool;
     int64_t page_bytes;
@@ -245,9 +245,11 @@ struct Feed {
     // of the token, or of the sequence's first page where it has none
     __device__ __forceinline__ int page_id() const { return ld_s32(table + (at < hi ? page : 0)); }
 
-    __device__ __forceinline__ void start(const PagedAttnParams &p, int seq, int head, int lo, int hi_, int tok_)
+    __device__ __forceinline__ void start(const PagedAttnParams &p, int seq, int head, int lo, int first_, int hi_,
+                                          int tok_)
     {
         tok = tok_;
+        first = first_;
         hi = hi_;
         at = lo + tok;
         page = (at >> 4) / p.groups;
@@ -265,7 +267,7 @@ struct Feed {
     // on to the next tile.
     __device__ __forceinline__ const uint8_t *step(const PagedAttnParams &p, bool &there)
     {
-        there = at < hi && id >= 0 && id < p.num_pages;
+        there = at >= first && at < hi && id >= 0 && id < p.num_pages;
         const uint8_t *g = there ? pool + id * page_bytes + in * kKVGroupBytes : p.workspace;
         at += kTile;
         page += pages;
@@ -346,9 +348,9 @@ paged_attn_tc_kernel(const PagedAttnParams p)
     const int b = sm.seq, head = blockIdx.x % p.hk;
     const Seq s = load_seq(p, b);
     const int row0 = sm.block * kRows, rows = min(kRows, s.nq * p.per - row0);
-    // keys that some row of the block sees: [lo, hi), in n tiles
+    // keys that some row of the block sees: [first, hi), in n tiles from lo
     const int i_last = (row0 + rows - 1) / p.per, hi = s.first_pos + i_last + 1;
-    const int lo = p.window > 0 ? max(0, s.first_pos + row0 / p.per - p.window + 1) & ~15 : 0;
+    const int first = p.window > 0 ? max(0, s.first_pos + row0 / p.per - p.window + 1) : 0, lo = first & ~15;
     const int n = hi > lo ? (hi - lo + kTile - 1) / kTile : 0;
 
     if (warp == 12) {
@@ -370,7 +372,7 @@ paged_attn_tc_kernel(const PagedAttnParams p)
     const bool real = row < rows;
     if (producer && n > 0) {  // (the branches are one, so that neither keeps registers for the other)
         bool there;
-        feed.start(p, b, head, lo, hi, threadIdx.x - 8 * 32);
+        feed.start(p, b, head, lo, first, hi, threadIdx.x - 8 * 32);
         const uint8_t *g = feed.step(p, there);
         feed.load(k, g, there, kKVCodesK, kKVScalesK);
         feed.load(v, g, there, kKVCodesV, kKVScalesV);

@@ -184,6 +184,33 @@ def test_decode_window(window):
     run_decode(Cache(2, LENS, 2, 16), 32, "fp16", window=window)
 
 
+def test_window_up_to_the_largest_int():
+    """A window past every length hides nothing, whatever the positions."""
+    c = Cache(33, [1, 2, 0, 90, 300], 2, 16)
+    run_decode(c, 4, "bf16", window=2 ** 31 - 1)
+    run_extend(c, 4, [9, 2, 40, 5, 20], "bf16", window=2 ** 31 - 1)
+    run_extend(c, 4, [900, 2, 40, 500, 300], "fp16", window=2 ** 31 - 4)
+
+
+@pytest.mark.parametrize("window", [1, 37, 100])
+@pytest.mark.parametrize("new", [1, 3, 150])
+def test_bytes_before_the_window_are_not_looked_at(window, new):
+    """Tokens that no query sees hold NaN scales (a page given to others)."""
+    c = Cache(34, [40, 200, 901, 1500], 2, 32)
+    new = [min(new, n) for n in c.lens]
+    flat = c.pool.reshape(c.pages, 2, 2, 2304)
+    for b, n in enumerate(c.lens):
+        for t in range(max(0, n - new[b] - window + 1)):
+            g, i = flat[c.table[b, t // 32], :, t % 32 // 16], t % 16
+            for base, size in ((0, 64), (1024, 64), (2048, 8), (2176, 8)):
+                g[:, base + i * size:base + (i + 1) * size] = 0xFF
+    c.dpool = torch.from_numpy(c.pool).cuda()
+    if max(new) == 1:
+        run_decode(c, 4, "bf16", window=window)
+        run_decode(c, 32, "fp16", window=window)
+    run_extend(c, 4, new, "fp16", window=window)
+
+
 def test_decode_one_long_sequence():
     """One sequence over every SM, 40,007 keys; one and two KV heads."""
     run_decode(Cache(3, [40007], 1, 64), 4, "fp16")
@@ -343,6 +370,22 @@ def test_starts_out_of_order_are_clamped():
                                       f32dev(GS_K), f32dev(GS_V), 0.1, out.t, ws)
         torch.cuda.synchronize()
         assert out.guards_intact()
+
+
+def test_workspaces_that_are_refused():
+    """One whose memory is not what its size says, too small, or none."""
+    c = Cache(35, [20], 1, 16)
+    q = torch.zeros((1, 2, D), dtype=torch.bfloat16, device="cuda")
+    n = rq.rq_paged_attn_nvfp4_workspace_bytes(2, 1)
+    for ws in (torch.empty(1, dtype=torch.uint8, device="cuda").expand(n),
+               torch.empty((n, 2), dtype=torch.uint8, device="cuda")[:, 0], None):
+        with pytest.raises(ValueError):
+            rq.rq_paged_decode_attn_nvfp4(q, c.dpool, 16, c.dtable, c.dlens, f32dev(1), f32dev(1), 0.1, q.clone(), ws)
+    with pytest.raises(rq.RQError):
+        rq.paged_decode_attn_nvfp4(q, c.dpool, 16, c.dtable, c.dlens, f32dev(1), f32dev(1), 0.1,
+                                   workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        rq.paged_decode_attn_nvfp4(q[0], c.dpool, 16, c.dtable, c.dlens, f32dev(1), f32dev(1), 0.1)
 
 
 def test_decode_equals_extend_by_one():

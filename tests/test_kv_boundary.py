@@ -90,7 +90,8 @@ COMMON = [
     (DTYPE, dict(dt=5)), (SHAPE, dict(n=-1)), (SHAPE, dict(hq=15)), (SHAPE, dict(hq=0)),
     (SHAPE, dict(hk=0)), (UNSUP, dict(d=96)), (SHAPE, dict(page=8)), (SHAPE, dict(pages=-2)),
     (SHAPE, dict(per=6)), (SHAPE, dict(per=-1)), (SHAPE, dict(scale=0.0)), (SHAPE, dict(scale=-1.0)),
-    (SHAPE, dict(scale=float("nan"))), (SHAPE, dict(window=-1)), (SHAPE, dict(bytes=1000)),
+    (SHAPE, dict(scale=float("nan"))), (SHAPE, dict(scale=float("inf"))), (SHAPE, dict(scale=3e38)),
+    (SHAPE, dict(window=-1)), (SHAPE, dict(bytes=1000)),
     (SHAPE, dict(per=1 << 25, stride=1 << 25)), (SHAPE, dict(qs=128)), (MISAL, dict(qs=16 * 128 + 1)),
     (NULL, dict(q=None)), (NULL, dict(pool=None)), (NULL, dict(table=None)), (NULL, dict(lens=None)),
     (NULL, dict(kg=None)), (NULL, dict(vg=None)), (NULL, dict(out=None)), (NULL, dict(ws=None)),
