@@ -568,8 +568,8 @@ paged_attn_split_kernel(const PagedAttnParams p)
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    PartInfo *info = reinterpret_cast<PartInfo *>(p.workspace) + 2 * blockIdx.x;
-    float *parts = reinterpret_cast<float *>(p.workspace + kInfoBytes) +
+    PartInfo *info = reinterpret_cast<PartInfo *>(p.workspace + kTakenBytes) + 2 * blockIdx.x;
+    float *parts = reinterpret_cast<float *>(p.workspace + kTakenBytes + kInfoBytes) +
                    (int64_t)blockIdx.x * 2 * kPartFloats<NT>;
 
     // ---- this CTA's share: units (head, block, chunk of keys) of all
@@ -610,6 +610,7 @@ paged_attn_split_kernel(const PagedAttnParams p)
         start_rem = rem;
     }
     if (threadIdx.x < 2) info[threadIdx.x].valid = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<unsigned *>(p.workspace) = 0;
     __syncthreads();
     if (u >= u_end) return;
     int b = start_seq;
@@ -738,7 +739,7 @@ paged_attn_join_kernel(const PagedAttnParams p, int ctas)
     __shared__ int last;
     pdl_trigger();
     pdl_wait();
-    const PartInfo *info = reinterpret_cast<const PartInfo *>(p.workspace);
+    const PartInfo *info = reinterpret_cast<const PartInfo *>(p.workspace + kTakenBytes);
     const int i = blockIdx.x;
     const PartInfo me = info[2 * i + 1];
     if (!me.valid) return;
@@ -748,7 +749,7 @@ paged_attn_join_kernel(const PagedAttnParams p, int ctas)
         if (info[2 * j].valid && info[2 * j].last) atomicMin(&last, j);
     __syncthreads();
     const int end = last, n = end - i + 1;
-    const float *parts = reinterpret_cast<const float *>(p.workspace + kInfoBytes);
+    const float *parts = reinterpret_cast<const float *>(p.workspace + kTakenBytes + kInfoBytes);
     auto part = [&](int k) {  // the k-th part of the item
         return parts + ((int64_t)(i + k) * 2 + (k == 0)) * kPartFloats<NT>;
     };
@@ -844,7 +845,7 @@ bool is_short(const PagedAttnParams &p, int dev)
 
 size_t paged_attn_workspace_bytes(int, int)
 {
-    return kInfoBytes + (size_t)kMaxCtas * 2 * kPartFloats<2> * sizeof(float);
+    return kTakenBytes + kInfoBytes + (size_t)kMaxCtas * 2 * kPartFloats<2> * sizeof(float);
 }
 
 template <typename DT>

@@ -79,6 +79,10 @@ __device__ __forceinline__ float lse_of(float m, float l)
     return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
+// The workspace begins with the number of the row blocks that the CTAs of the
+// tensor-memory kernel have taken, set to 0 by the split kernel before it.
+constexpr size_t kTakenBytes = 16;
+
 template <typename DT>
 cudaError_t launch_paged_attn_tc(const PagedAttnParams &p, cudaStream_t stream);
 

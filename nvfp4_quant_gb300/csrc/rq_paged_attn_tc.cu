@@ -35,19 +35,34 @@ namespace rq {
 namespace {
 
 constexpr int kD = 128, kTile = 128, kRows = 2 * kTile;
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 14 * 32;
 constexpr uint32_t kTileBytes = kTile * kD * 2;  // 32 KB
 // shared memory (from a 1024-byte boundary): Q0 Q1 K[2] V[2], then the small part
 constexpr uint32_t kQ = 0, kK = 2 * kTileBytes, kV = kK + 2 * kTileBytes, kSmall = kV + 2 * kTileBytes;
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
+struct TcParams : PagedAttnParams {
+    unsigned limit;  // row blocks, at most
+    int width;       // the window, or more than any sequence has
+};
+
+// A block of rows: its sequence and KV head, the rows row0 .. row0 + rows - 1 of
+// the sequence (none: there is no more work), and the keys [first, hi) that some
+// of them see, in n tiles from lo.
+struct Work {
+    int seq, head, q0, first_pos, row0, rows, lo, first, hi, n;
+};
+
 struct Small {
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2], drained;
-    uint32_t seen[4][4];  // tile j's readable tokens, ring of 4
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2], q_full[2], drained;
+    uint64_t work_full[2], work_empty[2], claim;
+    alignas(16) uint32_t seen[4][4];  // tile's readable tokens, ring of 4
+    Work work[2];
     uint32_t tmem;
     int failed;
-    int seq, block;
-    int64_t scan[13];
+    float k_gs, v_gs;
+    int64_t scan[14];
+    int64_t upto[kThreads];  // row blocks of the sequences up to the thread's last
 };
 constexpr size_t kSmemBytes = 1024 + kSmall + sizeof(Small);
 
@@ -114,7 +129,7 @@ __device__ __forceinline__ void tm_wait_ld(uint32_t (&v)[32])
                    "+r"(v[29]), "+r"(v[30]), "+r"(v[31])
                  :: "memory");
 }
-__device__ __forceinline__ void tm_store32(uint32_t addr, const uint32_t (&v)[32])
+__device__ __forceinline__ void tm_store32(uint32_t addr, const uint32_t *v)
 {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
@@ -125,16 +140,6 @@ __device__ __forceinline__ void tm_store32(uint32_t addr, const uint32_t (&v)[32
            "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
         : "memory");
 }
-__device__ __forceinline__ void tm_store16(uint32_t addr, const uint32_t *v)
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15, %16};"
-        :: "r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
-           "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
-}
-
 __device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count)
 {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(smem_addr(bar)), "r"(count) : "memory");
@@ -289,19 +294,60 @@ struct Feed {
 
 template <typename DT>
 __global__ void __launch_bounds__(kThreads, 1)
-paged_attn_tc_kernel(const PagedAttnParams p)
+paged_attn_tc_kernel(const TcParams p)
 {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     Small &sm = *reinterpret_cast<Small *>(smem + kSmall);
     pdl_trigger();
-    pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 
-    // ---- which rows: CTA x / hk in the order of the sequences' row blocks,
-    // the last (longest) block of a sequence first
+    if (threadIdx.x == 0) {
+        sm.failed = 0;
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&sm.k_full[i], 4);
+            bar_init(&sm.v_full[i], 4);
+            bar_init(&sm.k_empty[i], 1);
+            bar_init(&sm.v_empty[i], 1);
+            bar_init(&sm.s_full[i], 1);
+            bar_init(&sm.p_full[i], 4);
+            bar_init(&sm.pv_done[i], 1);
+            bar_init(&sm.q_full[i], 4);
+            bar_init(&sm.work_full[i], 1);
+            bar_init(&sm.work_empty[i], 13);
+        }
+        bar_init(&sm.claim, 1);
+        bar_init(&sm.drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
+                     :: "r"(smem_addr(&sm.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    pdl_wait();
+    if (threadIdx.x == 0) {
+        sm.k_gs = ld_f32(p.k_gs);
+        sm.v_gs = ld_f32(p.v_gs);
+        sm.work[0].rows = 0;
+    }
+    // The at-th row block of sequence b (the last, longest one first).
+    auto work_of = [&](int b, const Seq &s, int head, int at, Work &w) {
+        w.seq = b;
+        w.head = head;
+        w.q0 = s.q0;
+        w.first_pos = s.first_pos;
+        w.row0 = (row_blocks(p, s) - 1 - at) * kRows;
+        w.rows = min(kRows, s.nq * p.per - w.row0);
+        w.hi = s.first_pos + (w.row0 + w.rows - 1) / p.per + 1;
+        w.first = p.window > 0 ? max(0, s.first_pos + w.row0 / p.per - p.window + 1) : 0;
+        w.lo = w.first & ~15;
+        w.n = w.hi > w.lo ? (w.hi - w.lo + kTile - 1) / kTile : 0;
+    };
+    // ---- row blocks of the sequences before and in a thread's run of them; the
+    // CTA's first one
+    const int per_thread = (p.n_seqs + kThreads - 1) / kThreads;
     {
-        const int per_thread = (p.n_seqs + kThreads - 1) / kThreads;
         const int b0 = min(p.n_seqs, (int)threadIdx.x * per_thread), b1 = min(p.n_seqs, b0 + per_thread);
         int64_t mine = 0;
         for (int b = b0; b < b1; ++b) mine += row_blocks(p, load_seq(p, b));
@@ -312,134 +358,89 @@ paged_attn_tc_kernel(const PagedAttnParams p)
             if (lane >= o) upto += v;
         }
         if (lane == 31) sm.scan[warp] = upto;
-        if (threadIdx.x == 0) {
-            sm.seq = -1;
-            sm.failed = 0;
-            for (int i = 0; i < 2; ++i) {
-                bar_init(&sm.k_full[i], 4);
-                bar_init(&sm.v_full[i], 4);
-                bar_init(&sm.k_empty[i], 1);
-                bar_init(&sm.v_empty[i], 1);
-                bar_init(&sm.s_full[i], 1);
-                bar_init(&sm.p_full[i], 4);
-                bar_init(&sm.pv_done[i], 1);
-            }
-            bar_init(&sm.drained, 1);
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        }
         __syncthreads();
         for (int w = 0; w < warp; ++w) upto += sm.scan[w];
+        sm.upto[threadIdx.x] = upto;
         int64_t at = blockIdx.x / p.hk;
         if (upto - mine <= at && at < upto) {
             at -= upto - mine;
             for (int b = b0; b < b1; ++b) {
-                const int n = row_blocks(p, load_seq(p, b));
+                const Seq s = load_seq(p, b);
+                const int n = row_blocks(p, s);
                 if (at < n) {
-                    sm.seq = b;
-                    sm.block = n - 1 - (int)at;
+                    work_of(b, s, blockIdx.x % p.hk, (int)at, sm.work[0]);
                     break;
                 }
                 at -= n;
             }
         }
-        __syncthreads();
-        if (sm.seq < 0) return;
-    }
-    const int b = sm.seq, head = blockIdx.x % p.hk;
-    const Seq s = load_seq(p, b);
-    const int row0 = sm.block * kRows, rows = min(kRows, s.nq * p.per - row0);
-    // keys that some row of the block sees: [first, hi), in n tiles from lo
-    const int i_last = (row0 + rows - 1) / p.per, hi = s.first_pos + i_last + 1;
-    const int first = p.window > 0 ? max(0, s.first_pos + row0 / p.per - p.window + 1) : 0, lo = first & ~15;
-    const int n = hi > lo ? (hi - lo + kTile - 1) / kTile : 0;
-
-    if (warp == 12) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
-                     :: "r"(smem_addr(&sm.tmem)) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    // ---- the first keys and values are asked for before the queries
-    const bool producer = warp >= 8 && warp < 12;
-    Feed feed;
-    Row k, v;
-    // ---- queries: a warp its 32 rows, 16 lanes a row and all loads at once (a
-    // thread a row took 5.8 us here), times a power of two for bf16
-    float scale = 0.0f;
-    const int t = warp >> 2, r = threadIdx.x & 127;  // tile and row (warps 0-7)
-    const int row = t * kTile + r;                   // of the block
-    const int query = (row0 + row) / p.per, group_head = head * p.per + (row0 + row) - query * p.per;
-    const int64_t out_row = (int64_t)(s.q0 + query) * p.hq + group_head;
-    const bool real = row < rows;
-    if (producer && n > 0) {  // (the branches are one, so that neither keeps registers for the other)
-        bool there;
-        feed.start(p, b, head, lo, first, hi, threadIdx.x - 8 * 32);
-        const uint8_t *g = feed.step(p, there);
-        feed.load(k, g, there, kKVCodesK, kKVScalesK);
-        feed.load(v, g, there, kKVCodesV, kKVScalesV);
-    } else if (warp < 8) {
-        // rows past the last repeat the block's first one (a load under a
-        // condition would be waited for at once)
-        const int first_query = row0 / p.per, first_head = head * p.per + row0 - first_query * p.per;
-        const int64_t mine = (s.q0 + (real ? query : first_query)) * p.q_stride +
-                             (int64_t)(real ? group_head : first_head) * kD;
-        uint4 x[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int64_t at = __shfl_sync(0xFFFFFFFFu, mine, 2 * i + (lane >> 4));
-            x[i] = ld_keep16(static_cast<const uint8_t *>(p.q) + at * 2 + (lane & 15) * 16);
-        }
-        float back = 1.0f;  // of the thread's own row
-        if (std::is_same<DT, BF16>::value) {
-            // largest magnitudes, four rows' reductions side by side: bf16 bits
-            // without the sign order as the values
-#pragma unroll
-            for (int i0 = 0; i0 < 16; i0 += 4) {
-                uint32_t a[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 w = x[i0 + i];
-                    a[i] = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
-                                    __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
-                }
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) a[i] = __vmaxu2(a[i], __shfl_xor_sync(0xFFFFFFFFu, a[i], o));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 pw = row_power(__uint_as_float(max(a[i] << 16, a[i] & 0xFFFF0000u)));
-                    float e[8];
-                    unpack8<DT>(x[i0 + i], e);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) e[k] *= pw.x;
-                    x[i0 + i] = pack8<FP16>(e);
-                    const float other = __shfl_sync(0xFFFFFFFFu, pw.y, (lane & 1) * 16);
-                    back = (lane >> 1) == i0 + i ? other : back;
-                }
-            }
-        }
-        const uint32_t tile = smem_addr(smem) + kQ + t * kTileBytes + ((lane >> 3) & 1) * (kTileBytes / 2);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int to = (warp & 3) * 32 + 2 * i + (lane >> 4);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
-                         :: "r"(tile + to * 128 + (((lane & 7) ^ (to & 7)) << 4)), "r"(x[i].x), "r"(x[i].y),
-                            "r"(x[i].z), "r"(x[i].w) : "memory");
-        }
-        scale = fmaxf(p.scale * back / ld_f32(p.k_gs), kLeastScale);
-        async_proxy_fence();
     }
     tm_fence_before();
     __syncthreads();
     tm_fence_after();
     const uint32_t tmem = sm.tmem;
     struct {
-        uint32_t k_full, k_empty, v_full, v_empty, s_full, p_full, pv_done, drained;
-    } const bars = {smem_addr(sm.k_full), smem_addr(sm.k_empty), smem_addr(sm.v_full),  smem_addr(sm.v_empty),
-                    smem_addr(sm.s_full), smem_addr(sm.p_full),  smem_addr(sm.pv_done), smem_addr(&sm.drained)};
+        uint32_t k_full, k_empty, v_full, v_empty, s_full, p_full, pv_done, q_full, drained, work_full, work_empty;
+    } const bars = {smem_addr(sm.k_full), smem_addr(sm.k_empty), smem_addr(sm.v_full),    smem_addr(sm.v_empty),
+                    smem_addr(sm.s_full), smem_addr(sm.p_full),  smem_addr(sm.pv_done),   smem_addr(sm.q_full),
+                    smem_addr(&sm.drained), smem_addr(sm.work_full), smem_addr(sm.work_empty)};
     volatile int *failed = &sm.failed;
+    // The CTA's i-th block of rows (rows = 0: there is none), for all roles but
+    // the one that finds it.
+    auto take = [&](int i, Work &w) {
+        if (warp_wait(bars.work_full + 8 * (i & 1), (i >> 1) & 1, failed)) {
+            w = sm.work[i & 1];
+            __syncwarp();
+            if (lane == 0) bar_arrive(bars.work_empty + 8 * (i & 1));
+        } else {
+            w.rows = 0;
+        }
+    };
 
-    if (warp == 12) {
+    if (warp == 13) {
+        // ---------------------------------------------------------- work
+        // Blocks are taken from a counter that all CTAs share, each late in the
+        // one before, the last (longest) block of a sequence first.
+        bool more = sm.work[0].rows > 0;
+        if (lane == 0) bar_arrive(bars.work_full);
+        for (int i = 1; more; ++i) {
+            if (!warp_wait(smem_addr(&sm.claim), (i - 1) & 1, failed)) break;
+            if (i > 1 && !warp_wait(bars.work_empty + 8 * (i & 1), ((i >> 1) + 1) & 1, failed)) break;
+            unsigned id = 0;
+            if (lane == 0) id = gridDim.x + atomicAdd(reinterpret_cast<unsigned *>(p.workspace), 1u);
+            id = __shfl_sync(0xFFFFFFFFu, id, 0);
+            int64_t at = id / (unsigned)p.hk;
+            int run = 0;  // threads whose runs lie before the block
+#pragma unroll
+            for (int k = 0; k < kThreads / 32; ++k)
+                run += __popc(__ballot_sync(0xFFFFFFFFu, sm.upto[k * 32 + lane] <= at));
+            more = id < p.limit && run < kThreads;
+            if (more) {
+                if (run > 0) at -= sm.upto[run - 1];
+                const int end = min(p.n_seqs, (run + 1) * per_thread);
+                for (int b0 = run * per_thread; b0 < end; b0 += 32) {
+                    const Seq s = load_seq(p, min(b0 + lane, end - 1));
+                    const int mine = b0 + lane < end ? row_blocks(p, s) : 0;
+                    int64_t upto = mine;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                        if (lane >= o) upto += v;
+                    }
+                    if (upto - mine <= at && at < upto) {
+                        work_of(b0 + lane, s, id % (unsigned)p.hk, (int)(at - (upto - mine)), sm.work[i & 1]);
+                    }
+                    const int64_t all = __shfl_sync(0xFFFFFFFFu, upto, 31);
+                    if (at < all) break;
+                    at -= all;
+                }
+            } else if (lane == 0) {
+                sm.work[i & 1].rows = 0;
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(bars.work_full + 8 * (i & 1));
+        }
+    } else if (warp == 12) {
         // ---------------------------------------------------------- products
         // The whole warp walks the loop, one elected lane issues: addresses
         // and descriptors then stay in uniform registers (a loop in one lane
@@ -449,8 +450,8 @@ paged_attn_tc_kernel(const PagedAttnParams p)
         const uint64_t dq = operand(base + kQ, 16), dk = operand(base + kK, 16);
         const uint64_t dv = operand(base + kV, kTileBytes / 2);
         const bool lead = elect_one();
-        auto qk = [&](int tt, int j) {
-            const uint64_t a = dq + tt * (kTileBytes >> 4), bk = dk + (j & 1) * (kTileBytes >> 4);
+        auto qk = [&](int tt, int g) {
+            const uint64_t a = dq + tt * (kTileBytes >> 4), bk = dk + (g & 1) * (kTileBytes >> 4);
             if (lead) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
@@ -458,32 +459,41 @@ paged_attn_tc_kernel(const PagedAttnParams p)
                     mma_ss(tmem + kColS + tt * 128, a + off, bk + off, kIdescQK, k > 0);
                 }
                 mma_commit(bars.s_full + 8 * (tt));
-                if (tt == 1) mma_commit(bars.k_empty + 8 * (j & 1));
+                if (tt == 1) mma_commit(bars.k_empty + 8 * (g & 1));
             }
         };
-        bool ok = n > 0 && warp_wait(bars.k_full + 8 * (0), 0, failed);
-        if (ok) {
-            tm_fence_after();
-            qk(0, 0);
-            qk(1, 0);
-        }
-        for (int j = 0; ok && j < n; ++j) {
-            ok = warp_wait(bars.v_full + 8 * (j & 1), (j >> 1) & 1, failed) &&
-                 (j + 1 == n || warp_wait(bars.k_full + 8 * ((j + 1) & 1), ((j + 1) >> 1) & 1, failed));
-            const uint64_t bv = dv + (j & 1) * (kTileBytes >> 4);
+        bool ok = true;
+        int g = 0;  // tiles of keys so far
+        for (int i = 0; ok; ++i) {
+            Work w;
+            take(i, w);
+            if (w.rows == 0) break;
+            const int end = g + w.n;
+            ok = w.n == 0 || warp_wait(bars.k_full + 8 * (g & 1), (g >> 1) & 1, failed);
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
-                if (!ok || !(ok = warp_wait(bars.p_full + 8 * (tt), j & 1, failed))) break;
+                if (!ok || !(ok = warp_wait(bars.q_full + 8 * tt, i & 1, failed))) break;
                 tm_fence_after();
-                if (lead) {
+                if (w.n > 0) qk(tt, g);
+            }
+            for (bool more = false; ok && g < end; ++g, more = true) {
+                ok = warp_wait(bars.v_full + 8 * (g & 1), (g >> 1) & 1, failed) &&
+                     (g + 1 == end || warp_wait(bars.k_full + 8 * ((g + 1) & 1), ((g + 1) >> 1) & 1, failed));
+                const uint64_t bv = dv + (g & 1) * (kTileBytes >> 4);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_ts(tmem + kColO + tt * 128, tmem + kColS + tt * 128 + k * 8, bv + k * (2048 >> 4),
-                               kIdescPV, j > 0 || k > 0);
-                    mma_commit(bars.pv_done + 8 * (tt));
-                    if (tt == 1) mma_commit(bars.v_empty + 8 * (j & 1));
+                for (int tt = 0; tt < 2; ++tt) {
+                    if (!ok || !(ok = warp_wait(bars.p_full + 8 * tt, g & 1, failed))) break;
+                    tm_fence_after();
+                    if (lead) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_ts(tmem + kColO + tt * 128, tmem + kColS + tt * 128 + k * 8, bv + k * (2048 >> 4),
+                                   kIdescPV, more || k > 0);
+                        mma_commit(bars.pv_done + 8 * tt);
+                        if (tt == 1) mma_commit(bars.v_empty + 8 * (g & 1));
+                    }
+                    if (g + 1 < end) qk(tt, g + 1);
                 }
-                if (j + 1 < n) qk(tt, j + 1);
             }
         }
         // no product may outlive the operands and the tensor memory, also
@@ -491,176 +501,315 @@ paged_attn_tc_kernel(const PagedAttnParams p)
         int none = 0;
         if (lead) mma_commit(bars.drained);
         warp_wait(bars.drained, 0, &none);
-    } else if (producer) {
+    } else if (warp >= 8) {
         // ---------------------------------------------------------- keys and values
-        const int tok = feed.tok;
+        // The next tile's bytes are asked for before this one is decoded, on to
+        // the next block's first tile.
+        const int tok = threadIdx.x - 8 * 32;
         const uint32_t to = smem_addr(smem) + tok * 128 + ((tok & 7) << 4);
-        for (int j = 0; j < n; ++j) {
-            const int st = j & 1;
-            if (j >= 2 && !warp_wait(bars.k_empty + 8 * st, ((j >> 1) + 1) & 1, failed)) break;
-            const uint32_t seen = __ballot_sync(0xFFFFFFFFu, k.there);
-            if (lane == 0) sm.seen[j & 3][warp - 8] = seen;
-            decode_row(k, to + kK + st * kTileBytes);
-            async_proxy_fence();
-            __syncwarp();
-            if (lane == 0) bar_arrive(bars.k_full + 8 * st);
+        Feed feed;
+        Row k, v;
+        int i = 0, left = 1;  // left: tiles of the block not yet asked for, and one
+        auto next = [&]() {   // on to the next block with keys
+            Work w;
+            do take(i++, w);
+            while (w.rows > 0 && w.n == 0);
+            if (w.rows == 0) return false;
+            feed.start(p, w.seq, w.head, w.lo, w.first, w.hi, tok);
+            left = w.n;
+            return true;
+        };
+        for (int g = -1;; ++g) {  // (-1: nothing to decode yet)
+            const int st = g & 1;
+            if (g >= 0) {
+                if (g >= 2 && !warp_wait(bars.k_empty + 8 * st, ((g >> 1) + 1) & 1, failed)) break;
+                const uint32_t seen = __ballot_sync(0xFFFFFFFFu, k.there);
+                if (lane == 0) sm.seen[g & 3][warp - 8] = seen;
+                decode_row(k, to + kK + st * kTileBytes);
+                async_proxy_fence();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bars.k_full + 8 * st);
+            }
+            const bool more = --left > 0 || next();
+            if (!more && g < 0) break;
             bool there;
-            const uint8_t *g = feed.step(p, there);
-            feed.load(k, g, there, kKVCodesK, kKVScalesK);
-            if (j >= 2 && !warp_wait(bars.v_empty + 8 * st, ((j >> 1) + 1) & 1, failed)) break;
-            decode_row(v, to + kV + st * kTileBytes);
-            async_proxy_fence();
-            __syncwarp();
-            if (lane == 0) bar_arrive(bars.v_full + 8 * st);
-            feed.load(v, g, there, kKVCodesV, kKVScalesV);
+            const uint8_t *src = feed.step(p, there);
+            feed.load(k, src, there, kKVCodesK, kKVScalesK);
+            if (g >= 0) {
+                if (g >= 2 && !warp_wait(bars.v_empty + 8 * st, ((g >> 1) + 1) & 1, failed)) break;
+                decode_row(v, to + kV + st * kTileBytes);
+                async_proxy_fence();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bars.v_full + 8 * st);
+            }
+            if (!more) break;
+            feed.load(v, src, there, kKVCodesV, kKVScalesV);
         }
     } else {
-        // ---------------------------------------------------------- softmax
+        // ---------------------------------------------------------- rows
+        const int t = warp >> 2, r = threadIdx.x & 127;          // tile and row of it
+        const uint32_t tile = smem_addr(smem) + kQ + t * kTileBytes;
         const uint32_t at = tmem + ((uint32_t)(warp & 3) << 21);  // the warp's 32 rows
         const uint32_t s_at = at + kColS + t * 128, o_at = at + kColO + t * 128;
-        const int row_hi = real ? s.first_pos + query + 1 : 0;               // keys [row_lo, row_hi)
-        const int row_lo = p.window > 0 ? row_hi - p.window : 0;
-        const float v_gs = ld_f32(p.v_gs);
-        float m = kNoMax, l = 0.0f;
-        for (int j = 0; j < n; ++j) {
-            if (!warp_wait(bars.s_full + 8 * (t), j & 1, failed)) break;
-            tm_fence_after();
-            auto visible = [&](int c) {  // of the tile's columns 32 c ..
-                const int first = lo + j * kTile + 32 * c, below = row_hi - first, from = row_lo - first;
-                const uint32_t a = below >= 32 ? ~0u : (below <= 0 ? 0u : (1u << below) - 1u);
-                const uint32_t z = from <= 0 ? 0u : (from >= 32 ? ~0u : (1u << from) - 1u);
-                return a & ~z & sm.seen[j & 3][c];
-            };
-            uint32_t pk[64];
-            float sum[4] = {};
-            const float2 s2 = make_float2(scale, scale);
-            auto exps = [&](uint32_t (&x)[32], int c) {  // one chunk of P and of the sum
-                const uint32_t vis = visible(c);
-                if (__any_sync(0xFFFFFFFFu, vis != ~0u)) {
+        // Queries: a warp its 32 rows, 16 lanes a row and all loads at once (a
+        // thread a row took 5.8 us here); rows past the last repeat the block's
+        // first one (a load under a condition would be waited for at once).
+        uint4 x[16];
+        auto load_q = [&](const Work &w) {
+            const int row = w.row0 + (t * kTile + r < w.rows ? t * kTile + r : 0), query = row / p.per;
+            const int64_t mine = (w.q0 + query) * p.q_stride + (int64_t)(w.head * p.per + row - query * p.per) * kD;
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (!(vis & (1u << k))) x[k] = 0xFF800000u;  // -inf
-                }
-                // 16 at a time: the exponentials first, then what uses them
-                // (this file is compiled with little instruction scheduling,
-                // so that they stay apart: the scheduler's own order put each
-                // use behind its exponential and took 14 clocks an element of
-                // a lone warp where this takes 6.6)
-                const float2 nm = make_float2(-m, -m);
+            for (int i = 0; i < 16; ++i) {
+                const int64_t from = __shfl_sync(0xFFFFFFFFu, mine, 2 * i + (lane >> 4));
+                x[i] = ld_keep16(static_cast<const uint8_t *>(p.q) + from * 2 + (lane & 15) * 16);
+            }
+        };
+        // Into the tile, times a power of two for bf16; the scale of the row's
+        // scores.
+        auto put_q = [&]() {
+            float back = 1.0f;  // of the thread's own row
+            if (std::is_same<DT, BF16>::value) {
+                // Largest magnitudes (bf16 bits without the sign order as the
+                // values): the 16 lanes of a row hold 16 rows' partial ones, and
+                // halving both leaves lane i of them with row i's.
+                uint32_t a[8];
 #pragma unroll
-                for (int k0 = 0; k0 < 32; k0 += 16) {
-                    float y[16];
+                for (int k = 0; k < 8; ++k) {
+                    uint32_t two[2];
 #pragma unroll
-                    for (int k = 0; k < 16; k += 2) {
-                        const float2 z = __ffma2_rn(
-                            make_float2(__uint_as_float(x[k0 + k]), __uint_as_float(x[k0 + k + 1])), s2, nm);
-                        y[k] = ex2(z.x);
-                        y[k + 1] = ex2(z.y);
+                    for (int n = 0; n < 2; ++n) {
+                        const uint4 w = x[2 * k + n];
+                        two[n] = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                          __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
                     }
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) sum[k & 3] += y[k];
-#pragma unroll
-                    for (int k = 0; k < 16; k += 2) pk[16 * c + (k0 + k) / 2] = FP16::pack(y[k], y[k + 1]);
+                    a[k] = __vmaxu2(__byte_perm(two[0], two[1], 0x5410), __byte_perm(two[0], two[1], 0x7632));
                 }
-            };
-            auto all_exps = [&]() {  // the next chunk's scores arrive meanwhile
+#pragma unroll
+                for (int n = 4; n > 0; n >>= 1)
+#pragma unroll
+                    for (int k = 0; k < n; ++k) {
+                        const bool up = lane & (2 * n);
+                        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? a[k] : a[k + n], 2 * n);
+                        a[k] = __vmaxu2(up ? a[k + n] : a[k], got);
+                    }
+                a[0] = __vmaxu2(a[0], __shfl_xor_sync(0xFFFFFFFFu, a[0], 1));
+                const float2 pw = row_power(__uint_as_float(lane & 1 ? a[0] & 0xFFFF0000u : a[0] << 16));
+                back = __shfl_sync(0xFFFFFFFFu, pw.y, (lane & 1) * 16 + (lane >> 1));
+                float f[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[i] = __shfl_sync(0xFFFFFFFFu, pw.x, (lane & 16) + i);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float e[8];
+                    unpack8<DT>(x[i], e);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) e[k] *= f[i];
+                    x[i] = pack8<FP16>(e);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int to = (warp & 3) * 32 + 2 * i + (lane >> 4);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                             :: "r"(tile + ((lane >> 3) & 1) * (kTileBytes / 2) + to * 128 +
+                                    (((lane & 7) ^ (to & 7)) << 4)),
+                                "r"(x[i].x), "r"(x[i].y), "r"(x[i].z), "r"(x[i].w) : "memory");
+            }
+            async_proxy_fence();
+            __syncwarp();
+            if (lane == 0) bar_arrive(bars.q_full + 8 * t);
+            return fmaxf(p.scale * back / sm.k_gs, kLeastScale);
+        };
+
+        // (a block's numbers stay in shared memory: the loop over its keys has no
+        // register to spare)
+        bool more = warp_wait(bars.work_full, 0, failed) && sm.work[0].rows > 0;
+        float scale = 0.0f;
+        if (more) {
+            load_q(sm.work[0]);
+            scale = put_q();
+        }
+        int g = 0;  // tiles of keys so far
+        for (int i = 0; more; ++i) {
+            const Work &w = sm.work[i & 1];
+            // the row's keys [row_hi - width, row_hi), counted from lo less the
+            // tiles before
+            int row_hi = t * kTile + r < w.rows ? w.first_pos + (w.row0 + t * kTile + r) / p.per + 1 - w.lo : 0;
+            const int end = g + w.n;
+            // the next block is taken late, so that the last ones are shared out evenly
+            if (threadIdx.x == 0 && w.n == 0) bar_arrive(smem_addr(&sm.claim));
+            float m = kNoMax, l = 0.0f;
+            for (bool begun = false; g < end; ++g, begun = true, row_hi -= kTile) {
+                if (threadIdx.x == 0 && (begun ? end - g == 3 : end - g <= 3)) bar_arrive(smem_addr(&sm.claim));
+                bool full = __all_sync(0xFFFFFFFFu, row_hi >= kTile && row_hi <= p.width);
+                if (!warp_wait(bars.s_full + 8 * (t), g & 1, failed)) break;
+                tm_fence_after();
+                // nearly always every row sees the whole tile
+                const uint4 readable = *reinterpret_cast<const uint4 *>(sm.seen[g & 3]);
+                full = full && (readable.x & readable.y & readable.z & readable.w) == ~0u;
+                auto visible = [&](int c) {  // of the tile's columns 32 c ..
+                    const int below = row_hi - 32 * c, from = (int)((uint32_t)below - (uint32_t)p.width);
+                    const uint32_t a = below >= 32 ? ~0u : (below <= 0 ? 0u : (1u << below) - 1u);
+                    const uint32_t z = from <= 0 ? 0u : (from >= 32 ? ~0u : (1u << from) - 1u);
+                    return a & ~z & sm.seen[g & 3][c];
+                };
                 uint32_t x0[32], x1[32];
-                tm_load32(s_at, x0);
-                tm_wait_ld(x0);
-                tm_load32(s_at + 32, x1);
-                exps(x0, 0);
-                tm_wait_ld(x1);
-                tm_load32(s_at + 64, x0);
-                exps(x1, 1);
-                tm_wait_ld(x0);
-                tm_load32(s_at + 96, x1);
-                exps(x0, 2);
-                tm_wait_ld(x1);
-                exps(x1, 3);
-            };
-            if (j > 0) all_exps();  // (the first tile has no maximum yet)
-            if (j == 0 || __any_sync(0xFFFFFFFFu, sum[0] + sum[1] + sum[2] + sum[3] > kPMax)) {
-                // a row's maximum has risen: take it, rescale, and form P again
-                float top = m;
+                auto top_of = [&](int c0, int c1) {  // the largest score of columns 32 c0 .. (in x1)
+                    float top = kNoMax;
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t x[32];
-                    tm_load32(s_at + 32 * c, x);
-                    tm_wait_ld(x);
-                    const uint32_t vis = visible(c);
+                    for (int c = c0; c < c1; ++c) {
+                        tm_load32(s_at + 32 * c, x1);
+                        tm_wait_ld(x1);
+                        if (!full) {
+                            const uint32_t vis = visible(c);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if (vis & (1u << k)) top = fmaxf(top, __uint_as_float(x[k]) * scale);
-                }
-                const float f = ex2(m - top);
-                m = top;
-                l *= f;
-                if (j > 0) {
-                    if (!warp_wait(bars.pv_done + 8 * (t), (j - 1) & 1, failed)) break;
-                    tm_fence_after();
+                            for (int k = 0; k < 32; ++k)
+                                if (!(vis & (1u << k))) x1[k] = 0xFF800000u;
+                        }
+                        float a[4] = {top, kNoMax, kNoMax, kNoMax};
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) a[k & 3] = fmaxf(a[k & 3], __uint_as_float(x1[k]) * scale);
+                        top = fmaxf(fmaxf(a[0], a[1]), fmaxf(a[2], a[3]));
+                    }
+                    return top;
+                };
+                // (of a tile that all see, a quarter: those far above it take the path below)
+                if (!begun) m = top_of(0, full ? 1 : 4);
+                uint32_t pk[64];
+                float sum[4];
+                // (one copy of the code: instructions that miss their cache cost more
+                // than the branch)
+#pragma unroll 1
+                for (bool high = true;;) {
+                    sum[0] = sum[1] = sum[2] = sum[3] = 0.0f;
+                    const float2 s2 = make_float2(scale, scale), nm = make_float2(-m, -m);
+                    auto exps = [&](uint32_t (&x)[32], int c) {  // one chunk of P and of the sum
+                        if (!full) {
+                            const uint32_t vis = visible(c);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k)
+                                if (!(vis & (1u << k))) x[k] = 0xFF800000u;  // -inf
+                        }
+                        // 16 at a time: the exponentials first, then what uses them
+                        // (this file is compiled with little instruction scheduling,
+                        // so that they stay apart: the scheduler's own order put each
+                        // use behind its exponential and took 14 clocks an element of
+                        // a lone warp where this takes 6.6)
+#pragma unroll
+                        for (int k0 = 0; k0 < 32; k0 += 16) {
+                            float y[16];
+#pragma unroll
+                            for (int k = 0; k < 16; k += 2) {
+                                const float2 z = __ffma2_rn(
+                                    make_float2(__uint_as_float(x[k0 + k]), __uint_as_float(x[k0 + k + 1])), s2, nm);
+                                y[k] = ex2(z.x);
+                                y[k + 1] = ex2(z.y);
+                            }
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) sum[k & 3] += y[k];
+#pragma unroll
+                            for (int k = 0; k < 16; k += 2) pk[16 * c + (k0 + k) / 2] = FP16::pack(y[k], y[k + 1]);
+                        }
+                    };
+                    tm_load32(s_at, x0);  // the next chunk's scores arrive meanwhile
+                    tm_wait_ld(x0);
+                    tm_load32(s_at + 32, x1);
+                    exps(x0, 0);
+                    tm_wait_ld(x1);
+                    tm_load32(s_at + 64, x0);
+                    exps(x1, 1);
+                    tm_wait_ld(x0);
+                    tm_load32(s_at + 96, x1);
+                    exps(x0, 2);
+                    tm_wait_ld(x1);
+                    exps(x1, 3);
+                    if (!__any_sync(0xFFFFFFFFu, high && sum[0] + sum[1] + sum[2] + sum[3] > kPMax)) break;
+                    // a row's maximum has risen: take it, rescale, and form P again
+                    // (S was formed after the product of the tile before; the first
+                    // tile's product will replace O)
+                    const float top = fmaxf(m, top_of(0, 4));
+                    const float f = ex2(m - top);
+                    m = top;
+                    l *= f;
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t x[32];
-                        tm_load32(o_at + 32 * c, x);
-                        tm_wait_ld(x);
+                        tm_load32(o_at + 32 * c, x1);
+                        tm_wait_ld(x1);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * f);
-                        tm_store32(o_at + 32 * c, x);
+                        for (int k = 0; k < 32; ++k) x1[k] = __float_as_uint(__uint_as_float(x1[k]) * f);
+                        tm_store32(o_at + 32 * c, x1);
                     }
+                    high = false;
                 }
-                sum[0] = sum[1] = sum[2] = sum[3] = 0.0f;
-                all_exps();
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tm_store32(s_at, pk);
+                tm_store32(s_at + 32, pk + 32);
+                tm_wait_st();
+                tm_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(bars.p_full + 8 * t);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            // ------------------------------------------------------ last step
+            // the next block's queries on their way meanwhile
+            const bool told = warp_wait(bars.work_full + 8 * ((i + 1) & 1), ((i + 1) >> 1) & 1, failed);
+            more = told && sm.work[(i + 1) & 1].rows > 0;
+            load_q(sm.work[more ? (i + 1) & 1 : i & 1]);
+            if (w.n > 0) {
+                warp_wait(bars.pv_done + 8 * t, (end - 1) & 1, failed);
+                tm_fence_after();
+            }
+            // through the tile's place of Q, so that a row's 256 bytes leave together
+            const bool bad = *failed;
+            const float inv = bad ? __uint_as_float(0x7FC00000u) : out_factor(l, sm.v_gs);
+            const bool none = l == 0.0f && !bad;
+            auto put_out = [&](uint32_t (&y)[32], int c) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tm_store16(s_at + 16 * c, pk + 16 * c);
-            tm_wait_st();
-            tm_fence_before();
+                for (int k = 0; k < 32; k += 8) {
+                    float e[8];
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) e[n] = none ? 0.0f : __uint_as_float(y[k + n]) * inv;
+                    const uint4 v = pack8<DT>(e);
+                    const int chunk = 4 * c + k / 8;
+                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                                 :: "r"(tile + (chunk >> 3) * (kTileBytes / 2) + r * 128 +
+                                        (((chunk & 7) ^ (r & 7)) << 4)),
+                                    "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+                }
+            };
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t y[32];  // (of no meaning without keys: none is true then)
+                tm_load32(o_at + 32 * c, y);
+                tm_wait_ld(y);
+                put_out(y, c);
+            }
             __syncwarp();
-            if (lane == 0) bar_arrive(bars.p_full + 8 * (t));
-        }
-        // ---------------------------------------------------------- last step
-        if (n > 0) {
-            warp_wait(bars.pv_done + 8 * (t), (n - 1) & 1, failed);
-            tm_fence_after();
-        }
-        // through the tile's place of Q, so that a row's 256 bytes leave together
-        const bool bad = *failed;
-        const float inv = bad ? __uint_as_float(0x7FC00000u) : out_factor(l, v_gs);
-        const uint32_t tile = smem_addr(smem) + kQ + t * kTileBytes;
+            const int row = w.row0 + t * kTile + r, query = row / p.per;
+            const bool real = t * kTile + r < w.rows;
+            const int out_row = (w.q0 + query) * p.hq + w.head * p.per + row - query * p.per;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            uint32_t x[32] = {};
-            if (n > 0) {
-                tm_load32(o_at + 32 * c, x);
-                tm_wait_ld(x);
+            for (int n0 = 0; n0 < 16; n0 += 4) {
+                int to[4];
+                uint4 v[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    to[n] = __shfl_sync(0xFFFFFFFFu, real ? out_row : -1, 2 * (n0 + n) + (lane >> 4));
+                    const int from = (warp & 3) * 32 + 2 * (n0 + n) + (lane >> 4);
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v[n].x), "=r"(v[n].y), "=r"(v[n].z), "=r"(v[n].w)
+                                 : "r"(tile + ((lane >> 3) & 1) * (kTileBytes / 2) + from * 128 +
+                                       (((lane & 7) ^ (from & 7)) << 4)) : "memory");
+                }
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    if (to[n] >= 0)
+                        st16(static_cast<uint8_t *>(p.out) + (int64_t)to[n] * (kD * 2) + (lane & 15) * 16, v[n]);
             }
-#pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-                float e[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) e[i] = l == 0.0f && !bad ? 0.0f : __uint_as_float(x[k + i]) * inv;
-                const uint4 v = pack8<DT>(e);
-                const int chunk = 4 * c + k / 8;
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
-                             :: "r"(tile + (chunk >> 3) * (kTileBytes / 2) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4)),
-                                "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-            }
+            if (real && p.lse != nullptr) p.lse[out_row] = bad ? __uint_as_float(0x7FC00000u) : lse_of(m, l);
+            __syncwarp();
+            if (lane == 0) bar_arrive(bars.work_empty + 8 * (i & 1));
+            if (more) scale = put_q();
         }
-        __syncwarp();
-        const int64_t mine = real ? out_row : -1;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int64_t to = __shfl_sync(0xFFFFFFFFu, mine, 2 * i + (lane >> 4));
-            const int from = (warp & 3) * 32 + 2 * i + (lane >> 4);
-            uint4 v;
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                         : "r"(tile + ((lane >> 3) & 1) * (kTileBytes / 2) + from * 128 +
-                               (((lane & 7) ^ (from & 7)) << 4)) : "memory");
-            if (to >= 0) st16(static_cast<uint8_t *>(p.out) + to * (kD * 2) + (lane & 15) * 16, v);
-        }
-        if (real && p.lse != nullptr) p.lse[out_row] = bad ? __uint_as_float(0x7FC00000u) : lse_of(m, l);
     }
     // ---------------------------------------------------------------- leave
     tm_fence_before();
@@ -690,7 +839,13 @@ cudaError_t launch_paged_attn_tc(const PagedAttnParams &p, cudaStream_t stream)
     const int64_t rows = p.n_tokens * p.per;
     const int64_t blocks = rows / kRows + (rows / (p.few + 1) < p.n_seqs ? rows / (p.few + 1) : p.n_seqs);
     if (blocks * p.hk > INT32_MAX) return cudaErrorInvalidConfiguration;
-    return blocks > 0 ? launch_pdl(kern, (unsigned)(blocks * p.hk), kThreads, kSmemBytes, stream, p) : cudaSuccess;
+    if (blocks == 0) return cudaSuccess;
+    TcParams tp;
+    static_cast<PagedAttnParams &>(tp) = p;
+    tp.limit = (unsigned)(blocks * p.hk);
+    tp.width = p.window > 0 ? p.window : 1 << 30;
+    const unsigned sms = (unsigned)device_sms(dev);
+    return launch_pdl(kern, tp.limit < sms ? tp.limit : sms, kThreads, kSmemBytes, stream, tp);
 }
 
 template cudaError_t launch_paged_attn_tc<BF16>(const PagedAttnParams &, cudaStream_t);
