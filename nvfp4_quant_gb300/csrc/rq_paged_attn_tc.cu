@@ -189,6 +189,15 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
     return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, failed));
 }
 
+// Whether it is over already.
+__device__ __forceinline__ bool warp_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                 : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+    return __all_sync(0xFFFFFFFFu, done);
+}
+
 // Row tiles of the sequence for this kernel.
 __device__ __forceinline__ int row_blocks(const PagedAttnParams &p, const Seq &s)
 {
@@ -463,19 +472,21 @@ paged_attn_tc_kernel(const TcParams p)
             }
         };
         bool ok = true;
-        int g = 0;  // tiles of keys so far
+        int g = 0, q = 0;  // tiles of keys, blocks with keys so far
         for (int i = 0; ok; ++i) {
             Work w;
             take(i, w);
             if (w.rows == 0) break;
+            if (w.n == 0) continue;
             const int end = g + w.n;
-            ok = w.n == 0 || warp_wait(bars.k_full + 8 * (g & 1), (g >> 1) & 1, failed);
+            ok = warp_wait(bars.k_full + 8 * (g & 1), (g >> 1) & 1, failed);
 #pragma unroll
             for (int tt = 0; tt < 2; ++tt) {
-                if (!ok || !(ok = warp_wait(bars.q_full + 8 * tt, i & 1, failed))) break;
+                if (!ok || !(ok = warp_wait(bars.q_full + 8 * tt, q & 1, failed))) break;
                 tm_fence_after();
-                if (w.n > 0) qk(tt, g);
+                qk(tt, g);
             }
+            ++q;
             for (bool more = false; ok && g < end; ++g, more = true) {
                 ok = warp_wait(bars.v_full + 8 * (g & 1), (g >> 1) & 1, failed) &&
                      (g + 1 == end || warp_wait(bars.k_full + 8 * ((g + 1) & 1), ((g + 1) >> 1) & 1, failed));
@@ -503,25 +514,29 @@ paged_attn_tc_kernel(const TcParams p)
         warp_wait(bars.drained, 0, &none);
     } else if (warp >= 8) {
         // ---------------------------------------------------------- keys and values
-        // The next tile's bytes are asked for before this one is decoded, on to
-        // the next block's first tile.
+        // The next tile's bytes are asked for before this one is decoded; the next
+        // block's first ones as well, if the block is known by then.
         const int tok = threadIdx.x - 8 * 32;
         const uint32_t to = smem_addr(smem) + tok * 128 + ((tok & 7) << 4);
         Feed feed;
         Row k, v;
-        int i = 0, left = 1;  // left: tiles of the block not yet asked for, and one
-        auto next = [&]() {   // on to the next block with keys
+        int i = 0, g = 0, left = 1;        // left: tiles of the block not yet asked for, and one
+        bool ready = false, ended = false;  // a tile is in k and v; no block is left
+        auto begin = [&](bool wait) {       // on to the next block with keys
             Work w;
-            do take(i++, w);
-            while (w.rows > 0 && w.n == 0);
-            if (w.rows == 0) return false;
+            do {
+                if (!wait && !warp_test(bars.work_full + 8 * (i & 1), (i >> 1) & 1)) return false;
+                take(i++, w);
+            } while (w.rows > 0 && w.n == 0);
+            ended = w.rows == 0;
+            if (ended) return false;
             feed.start(p, w.seq, w.head, w.lo, w.first, w.hi, tok);
             left = w.n;
             return true;
         };
-        for (int g = -1;; ++g) {  // (-1: nothing to decode yet)
+        for (;;) {
             const int st = g & 1;
-            if (g >= 0) {
+            if (ready) {
                 if (g >= 2 && !warp_wait(bars.k_empty + 8 * st, ((g >> 1) + 1) & 1, failed)) break;
                 const uint32_t seen = __ballot_sync(0xFFFFFFFFu, k.there);
                 if (lane == 0) sm.seen[g & 3][warp - 8] = seen;
@@ -530,20 +545,25 @@ paged_attn_tc_kernel(const TcParams p)
                 __syncwarp();
                 if (lane == 0) bar_arrive(bars.k_full + 8 * st);
             }
-            const bool more = --left > 0 || next();
-            if (!more && g < 0) break;
+            // waits for the next block only with nothing left to decode: it may be
+            // told after the last tile's use
+            bool have = --left > 0;
+            if (!have && !ended) have = begin(!ready);
+            if (!have && !ready) break;
             bool there;
-            const uint8_t *src = feed.step(p, there);
+            const uint8_t *src = feed.step(p, there);  // (without one: of no use)
             feed.load(k, src, there, kKVCodesK, kKVScalesK);
-            if (g >= 0) {
+            if (ready) {
                 if (g >= 2 && !warp_wait(bars.v_empty + 8 * st, ((g >> 1) + 1) & 1, failed)) break;
                 decode_row(v, to + kV + st * kTileBytes);
                 async_proxy_fence();
                 __syncwarp();
                 if (lane == 0) bar_arrive(bars.v_full + 8 * st);
+                ++g;
             }
-            if (!more) break;
             feed.load(v, src, there, kKVCodesV, kKVScalesV);
+            ready = have;
+            if (!have) left = 1;
         }
     } else {
         // ---------------------------------------------------------- rows
@@ -627,7 +647,7 @@ paged_attn_tc_kernel(const TcParams p)
         float scale = 0.0f;
         if (more) {
             load_q(sm.work[0]);
-            scale = put_q();
+            if (sm.work[0].n > 0) scale = put_q();
         }
         int g = 0;  // tiles of keys so far
         for (int i = 0; more; ++i) {
@@ -808,7 +828,7 @@ paged_attn_tc_kernel(const TcParams p)
             if (real && p.lse != nullptr) p.lse[out_row] = bad ? __uint_as_float(0x7FC00000u) : lse_of(m, l);
             __syncwarp();
             if (lane == 0) bar_arrive(bars.work_empty + 8 * (i & 1));
-            if (more) scale = put_q();
+            if (more && sm.work[(i + 1) & 1].n > 0) scale = put_q();
         }
     }
     // ---------------------------------------------------------------- leave

@@ -352,6 +352,28 @@ def test_extend_long_chunk():
     run_extend(Cache(11, [2500, 600], 2, 16), 4, [700, 600], "fp16", window=600)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_extend_more_blocks_than_sms(dt):
+    """Blocks after one another on an SM, many of them without a key."""
+    run_extend(Cache(37, [40, 700, 0, 300], 1, 16), 16, [3000, 600, 70, 1000], dt)
+    run_extend(Cache(38, [1000, 5, 1500], 4, 32), 32, [1000, 900, 700], dt, window=333)
+
+
+@pytest.mark.parametrize("lens, new, hq, hk, dt, window", [
+    ([9600], [600], 8, 1, "bf16", 0), ([5000, 3], [300, 3], 16, 1, "fp16", 3000),
+    ([8300, 4100, 700], [333, 129, 600], 16, 1, "bf16", 0), ([2500], [2400], 8, 2, "fp16", 0)])
+def test_extend_few_blocks_of_many_keys(lens, new, hq, hk, dt, window):
+    """Blocks of rows whose keys several SMs share: joined, the same each time,
+    and with pages that cannot be read."""
+    c = Cache(36, lens, hk, 64)
+    a = run_extend(c, hq, new, dt, window=window)
+    assert np.array_equal(a, run_extend(c, hq, new, dt, window=window))
+    table = c.table.copy()
+    table[0, 1::3] = -1
+    table[0, 20:36] = -1
+    run_extend(c, hq, new, dt, window=window, table=table)
+
+
 @pytest.mark.parametrize("max_q", [0, 1, 7, 100000])
 def test_max_q_len_is_a_hint(max_q):
     """The bound chooses kernels; whatever it says, the results are right."""
