@@ -70,6 +70,9 @@ struct PartInfo {
     int valid, last, seq, head, block;
 };
 
+static_assert(kSharedBlocks * kSharedPartBytes <= (size_t)kMaxCtas * 2 * kPartFloats<2> * sizeof(float),
+              "the parts of the other kernel lie where this one's are");
+
 constexpr size_t kInfoBytes = ((size_t)kMaxCtas * 2 * sizeof(PartInfo) + 15) / 16 * 16;
 
 // Shared memory at a 32-bit address plus a constant (an address that goes
@@ -610,7 +613,8 @@ paged_attn_split_kernel(const PagedAttnParams p)
         start_rem = rem;
     }
     if (threadIdx.x < 2) info[threadIdx.x].valid = 0;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *reinterpret_cast<unsigned *>(p.workspace) = 0;
+    if (blockIdx.x == 0)
+        for (size_t i = threadIdx.x; i < kTakenBytes / 4; i += kThreads) reinterpret_cast<unsigned *>(p.workspace)[i] = 0;
     __syncthreads();
     if (u >= u_end) return;
     int b = start_seq;
@@ -875,7 +879,7 @@ cudaError_t launch_paged_attn(const PagedAttnParams &p, cudaStream_t stream)
                                                 : launch_split<DT, 2>(few, dev, stream);
     few.few = kFewColumns;
     e = launch_split<DT, 2>(few, dev, stream);
-    return e != cudaSuccess ? e : launch_paged_attn_tc<DT>(few, stream);
+    return e != cudaSuccess ? e : launch_paged_attn_tc<DT>(few, kInfoBytes, stream);
 }
 
 template cudaError_t launch_paged_attn<BF16>(const PagedAttnParams &, cudaStream_t);

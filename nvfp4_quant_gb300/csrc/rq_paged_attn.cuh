@@ -79,11 +79,14 @@ __device__ __forceinline__ float lse_of(float m, float l)
     return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
 }
 
-// The workspace begins with the number of the row blocks that the CTAs of the
-// tensor-memory kernel have taken, set to 0 by the split kernel before it.
-constexpr size_t kTakenBytes = 16;
+// The workspace begins with counters of the tensor-memory kernel, set to 0 by the
+// split kernel before it: the row blocks that its CTAs have taken, and the parts
+// that are there of each block that several CTAs share, per warp.
+constexpr int kSharedBlocks = 128;  // and parts of them; a part is 256 rows of O, m and l
+constexpr size_t kTakenBytes = 16 + kSharedBlocks * 8 * sizeof(unsigned);
+constexpr size_t kSharedPartBytes = 256 * 130 * sizeof(float);
 
 template <typename DT>
-cudaError_t launch_paged_attn_tc(const PagedAttnParams &p, cudaStream_t stream);
+cudaError_t launch_paged_attn_tc(const PagedAttnParams &p, size_t parts_at, cudaStream_t stream);
 
 }  // namespace rq

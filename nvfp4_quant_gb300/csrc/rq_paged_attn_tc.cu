@@ -1,18 +1,21 @@
 // rq_paged_attn_tc.cu -- attention over the paged NVFP4 cache for runs of
 // queries (prompts, chunks), on the fifth-generation tensor cores.
 //
-// A CTA takes 256 rows (query, head of the KV head's group) of a sequence as
-// two tiles of 128 and walks the keys in tiles of 128.  Per tile of keys:
+// A CTA takes blocks of 256 rows (query, head of the KV head's group) of a
+// sequence, one after another, as two tiles of 128 and walks the keys in tiles
+// of 128.  Per tile of keys:
 //   S_t = Q_t K^T        tcgen05.mma, both operands in shared memory,
 //   P_t = 2^(S_t c - m)  a thread a row, from and to tensor memory (the fp16 P
 //                        over S's own columns),
 //   O_t += P_t V         tcgen05.mma, P from tensor memory, V from shared,
 // with S and O of both tiles in all 512 tensor-memory columns.  Roles:
-//   warps 0-3, 4-7   the rows of tile 0, tile 1: softmax, and the last step
+//   warps 0-3, 4-7   the rows of tile 0, tile 1: softmax, the last step, and the
+//                    next block's queries
 //   warps 8-11       a token each: codes from global memory (one tile ahead in
 //                    registers), decoded to fp16 rows in shared memory
 //   warp 12          issues the products: PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1),
 //                    so that one tile's softmax runs under the other's products
+//   warp 13          finds the next block (a counter that all CTAs share)
 // m is the row's maximum when it was last looked at.  That is when a tile's sum
 // of P passes kPMax (so no P exceeds it, and fp16 holds them all): the row's O
 // is then rescaled in tensor memory, after the product before.  Between, no
@@ -21,10 +24,20 @@
 // What bounds it: 4 * 128 flops a visible pair on the tensor cores.  The
 // operands of a 128 x 128 x 16 product are 8 KB of shared memory in its 64
 // clocks (4 KB with P in tensor memory), the decoded tile another 32 bytes a
-// clock, and the exponentials need half the time of the products.
+// clock, and the exponentials need half the time of the products.  A tile takes
+// about 2830 clocks where its products take 2048: S waits for the product with V
+// and its own (1330 clocks with the signals), P for the softmax (1500).  With
+// neither exponentials nor decoding it still takes 2500.  8192 tokens of 32 + 8
+// heads: 382 us, 1440 TFLOP/s.
+//
+// A block begins and ends in about 9000 clocks (queries 2500, first maximum 400,
+// output 4500); one CTA a block, with its own start, took 12,000 more (8 prompts of
+// 1024 tokens 58 us, 55 like this).  Instruction caches are short for so much
+// straight code: code that few tiles need is kept out of the loop over the keys
+// (with the masks inline a tile took 3100 clocks).
 //
 // Every wait has a time limit (kWaitNs): past it the CTA gives up, writes NaN
-// and leaves, tensor memory freed.  No valid call meets it.
+// for its block and leaves, tensor memory freed.  No valid call meets it.
 #include "rq_paged_attn.cuh"
 
 #include <atomic>
@@ -39,18 +52,21 @@ constexpr int kThreads = 14 * 32;
 constexpr uint32_t kTileBytes = kTile * kD * 2;  // 32 KB
 // shared memory (from a 1024-byte boundary): Q0 Q1 K[2] V[2], then the small part
 constexpr uint32_t kQ = 0, kK = 2 * kTileBytes, kV = kK + 2 * kTileBytes, kSmall = kV + 2 * kTileBytes;
+constexpr int kPartTiles = 8;  // tiles of keys that a part has at least
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
 struct TcParams : PagedAttnParams {
     unsigned limit;  // row blocks, at most
     int width;       // the window, or more than any sequence has
+    size_t parts_at; // of the parts, behind the counters
 };
 
 // A block of rows: its sequence and KV head, the rows row0 .. row0 + rows - 1 of
 // the sequence (none: there is no more work), and the keys [first, hi) that some
-// of them see, in n tiles from lo.
+// of them see, in n tiles from lo; or one of the parts of a block whose keys
+// several CTAs share (parts 0: the others have it all).
 struct Work {
-    int seq, head, q0, first_pos, row0, rows, lo, first, hi, n;
+    int seq, head, q0, first_pos, row0, rows, lo, first, hi, n, parts, shared, slot;
 };
 
 struct Small {
@@ -155,8 +171,9 @@ __device__ __forceinline__ unsigned long long now_ns()
     return t;
 }
 // Waits until the barrier's phase of the given parity is over; gives up after
-// kWaitNs, or when another role of the CTA has (false).
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *failed)
+// a time, or when another role of the CTA has (false).
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile int *failed,
+                                         unsigned long long limit)
 {
     unsigned long long start = 0;
     for (uint32_t n = 0;; ++n) {
@@ -168,7 +185,7 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, volatile
             if (*failed) return false;
             const unsigned long long t = now_ns();
             if (start == 0) start = t;
-            if (t - start > kWaitNs) {
+            if (t - start > limit) {
                 *failed = 1;
                 return false;
             }
@@ -184,9 +201,10 @@ __device__ __forceinline__ bool elect_one()
 }
 
 // The same for a whole warp: every lane gets one answer.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *failed)
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *failed,
+                                          unsigned long long limit = kWaitNs)
 {
-    return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, failed));
+    return __all_sync(0xFFFFFFFFu, bar_wait(bar, parity, failed, limit));
 }
 
 // Whether it is over already.
@@ -301,7 +319,89 @@ struct Feed {
     }
 };
 
+// 32 channels of a row's sums into the tile as the output's.
 template <typename DT>
+__device__ __forceinline__ void put_out(uint32_t tile, int r, int c, const uint32_t (&y)[32], float inv)
+{
+#pragma unroll
+    for (int k = 0; k < 32; k += 8) {
+        float e[8];
+#pragma unroll
+        for (int n = 0; n < 8; ++n) e[n] = inv == 0.0f ? 0.0f : __uint_as_float(y[k + n]) * inv;
+        const uint4 v = pack8<DT>(e);
+        const int chunk = 4 * c + k / 8;
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
+                     :: "r"(tile + (chunk >> 3) * (kTileBytes / 2) + r * 128 + (((chunk & 7) ^ (r & 7)) << 4)),
+                        "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+    }
+}
+
+// A part of a block whose keys several CTAs share: a row's O, m and l go to
+// the workspace (4 channels of all rows together).  The warp that finds all the
+// others' there joins them in the order of the keys and puts the output into the
+// tile.  (Not inline: the kernel's main loop has no register to spare.)
+struct Joined {
+    float m, l;
+    bool last;
+};
+template <typename DT>
+__device__ __noinline__ Joined share_part(uint8_t *part0, unsigned *there, int mine, int parts, int row, uint32_t o_at,
+                                          uint32_t tile, int r, float m, float l, float v_gs)
+{
+    constexpr int kPart = kSharedPartBytes / sizeof(float4);
+    float4 *const rows0 = reinterpret_cast<float4 *>(part0) + row;
+    float2 *const ml0 = reinterpret_cast<float2 *>(reinterpret_cast<float4 *>(part0) + 32 * kRows) + row;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t y[32];
+        tm_load32(o_at + 32 * c, y);
+        tm_wait_ld(y);
+#pragma unroll
+        for (int k = 0; k < 32; k += 4)
+            __stcg(rows0 + mine * kPart + (8 * c + k / 4) * kRows,
+                   l == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                             : make_float4(__uint_as_float(y[k]), __uint_as_float(y[k + 1]),
+                                           __uint_as_float(y[k + 2]), __uint_as_float(y[k + 3])));
+    }
+    __stcg(ml0 + mine * (2 * kPart), make_float2(m, l));
+    __threadfence();
+    __syncwarp();
+    unsigned before = 0;
+    if ((threadIdx.x & 31) == 0) before = atomicAdd(there, 1u);
+    Joined j = {m, l, __shfl_sync(0xFFFFFFFFu, before, 0) == (unsigned)parts - 1};
+    if (!j.last) return j;
+    __threadfence();
+    j.m = kNoMax;
+    j.l = 0.0f;
+    for (int n = 0; n < parts; ++n) j.m = fmaxf(j.m, __ldcg(ml0 + n * (2 * kPart)).x);
+    for (int n = 0; n < parts; ++n) {
+        const float2 ml = __ldcg(ml0 + n * (2 * kPart));
+        j.l = fmaf(ex2(ml.x - j.m), ml.y, j.l);
+    }
+    const float inv = out_factor(j.l, v_gs);
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        uint32_t y[32] = {};
+#pragma unroll 1
+        for (int n = 0; n < parts; ++n) {
+            const float f = ex2(__ldcg(ml0 + n * (2 * kPart)).x - j.m);
+            float4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = __ldcg(rows0 + n * kPart + (8 * c + k) * kRows);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                y[4 * k] = __float_as_uint(fmaf(f, v[k].x, __uint_as_float(y[4 * k])));
+                y[4 * k + 1] = __float_as_uint(fmaf(f, v[k].y, __uint_as_float(y[4 * k + 1])));
+                y[4 * k + 2] = __float_as_uint(fmaf(f, v[k].z, __uint_as_float(y[4 * k + 2])));
+                y[4 * k + 3] = __float_as_uint(fmaf(f, v[k].w, __uint_as_float(y[4 * k + 3])));
+            }
+        }
+        put_out<DT>(tile, r, c, y, inv);
+    }
+    return j;
+}
+
+template <typename DT, bool SHARE>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_tc_kernel(const TcParams p)
 {
@@ -340,8 +440,14 @@ paged_attn_tc_kernel(const TcParams p)
         sm.v_gs = ld_f32(p.v_gs);
         sm.work[0].rows = 0;
     }
-    // The at-th row block of sequence b (the last, longest one first).
-    auto work_of = [&](int b, const Seq &s, int head, int at, Work &w) {
+    // Work in order: heads, a sequence's row blocks from its last (longest) one
+    // on, sequences.  The blocks left over from whole waves of CTAs are cut by keys
+    // into parts for all.
+    unsigned whole = 0, parts = 1, total = 0;  // blocks not cut, parts of the others, works
+    auto block_of = [&](unsigned id) { return !SHARE || id < whole ? id : whole + (id - whole) / parts; };
+    // Work `id`: the at-th row block of sequence b, or a part of it.
+    auto work_of = [&](unsigned id, int b, const Seq &s, int at, Work &w) {
+        const int head = block_of(id) % (unsigned)p.hk;
         w.seq = b;
         w.head = head;
         w.q0 = s.q0;
@@ -352,6 +458,19 @@ paged_attn_tc_kernel(const TcParams p)
         w.first = p.window > 0 ? max(0, s.first_pos + w.row0 / p.per - p.window + 1) : 0;
         w.lo = w.first & ~15;
         w.n = w.hi > w.lo ? (w.hi - w.lo + kTile - 1) / kTile : 0;
+        w.parts = 1;
+        if (SHARE && id >= whole && parts > 1) {
+            const int part = (id - whole) % parts, n = w.n;
+            if (n >= kPartTiles * (int)parts) {
+                w.lo += n * part / (int)parts * kTile;
+                w.n = n * (part + 1) / (int)parts - n * part / (int)parts;
+                w.parts = parts;
+                w.shared = (id - whole) / parts;
+                w.slot = id - whole;
+            } else if (part > 0) {
+                w.n = w.parts = 0;
+            }
+        }
     };
     // ---- row blocks of the sequences before and in a thread's run of them; the
     // CTA's first one
@@ -359,7 +478,12 @@ paged_attn_tc_kernel(const TcParams p)
     {
         const int b0 = min(p.n_seqs, (int)threadIdx.x * per_thread), b1 = min(p.n_seqs, b0 + per_thread);
         int64_t mine = 0;
-        for (int b = b0; b < b1; ++b) mine += row_blocks(p, load_seq(p, b));
+        bool longer = false;  // some block may have keys for several parts
+        for (int b = b0; b < b1; ++b) {
+            const Seq s = load_seq(p, b);
+            mine += row_blocks(p, s);
+            if (SHARE) longer |= min(s.hi, p.width) >= 2 * kPartTiles * kTile - kRows;
+        }
         int64_t upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -367,17 +491,29 @@ paged_attn_tc_kernel(const TcParams p)
             if (lane >= o) upto += v;
         }
         if (lane == 31) sm.scan[warp] = upto;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) upto += sm.scan[w];
+        if (SHARE)
+            longer = __syncthreads_or(longer);
+        else
+            __syncthreads();
+        int64_t blocks = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w == warp) upto += blocks;
+            blocks += sm.scan[w];
+        }
         sm.upto[threadIdx.x] = upto;
-        int64_t at = blockIdx.x / p.hk;
+        blocks = min(blocks * p.hk, (int64_t)p.limit);
+        const unsigned over = SHARE ? (unsigned)blocks % gridDim.x : 0;
+        whole = (unsigned)blocks - over;
+        parts = longer && over > 0 ? max(1u, min(8u, min(gridDim.x, (unsigned)kSharedBlocks) / max(over, 1u))) : 1;
+        total = whole + over * parts;
+        int64_t at = blockIdx.x < total ? block_of(blockIdx.x) / p.hk : INT64_MAX;
         if (upto - mine <= at && at < upto) {
             at -= upto - mine;
             for (int b = b0; b < b1; ++b) {
                 const Seq s = load_seq(p, b);
                 const int n = row_blocks(p, s);
                 if (at < n) {
-                    work_of(b, s, blockIdx.x % p.hk, (int)at, sm.work[0]);
+                    work_of(blockIdx.x, b, s, (int)at, sm.work[0]);
                     break;
                 }
                 at -= n;
@@ -413,17 +549,18 @@ paged_attn_tc_kernel(const TcParams p)
         bool more = sm.work[0].rows > 0;
         if (lane == 0) bar_arrive(bars.work_full);
         for (int i = 1; more; ++i) {
-            if (!warp_wait(smem_addr(&sm.claim), (i - 1) & 1, failed)) break;
+            // (the only wait for more than a tile's time)
+            if (!warp_wait(smem_addr(&sm.claim), (i - 1) & 1, failed, (sm.work[(i - 1) & 1].n + 1) * kWaitNs)) break;
             if (i > 1 && !warp_wait(bars.work_empty + 8 * (i & 1), ((i >> 1) + 1) & 1, failed)) break;
             unsigned id = 0;
             if (lane == 0) id = gridDim.x + atomicAdd(reinterpret_cast<unsigned *>(p.workspace), 1u);
             id = __shfl_sync(0xFFFFFFFFu, id, 0);
-            int64_t at = id / (unsigned)p.hk;
+            more = id < total;
+            int64_t at = more ? block_of(id) / (unsigned)p.hk : 0;
             int run = 0;  // threads whose runs lie before the block
 #pragma unroll
             for (int k = 0; k < kThreads / 32; ++k)
                 run += __popc(__ballot_sync(0xFFFFFFFFu, sm.upto[k * 32 + lane] <= at));
-            more = id < p.limit && run < kThreads;
             if (more) {
                 if (run > 0) at -= sm.upto[run - 1];
                 const int end = min(p.n_seqs, (run + 1) * per_thread);
@@ -437,7 +574,7 @@ paged_attn_tc_kernel(const TcParams p)
                         if (lane >= o) upto += v;
                     }
                     if (upto - mine <= at && at < upto) {
-                        work_of(b0 + lane, s, id % (unsigned)p.hk, (int)(at - (upto - mine)), sm.work[i & 1]);
+                        work_of(id, b0 + lane, s, (int)(at - (upto - mine)), sm.work[i & 1]);
                     }
                     const int64_t all = __shfl_sync(0xFFFFFFFFu, upto, 31);
                     if (at < all) break;
@@ -667,25 +804,31 @@ paged_attn_tc_kernel(const TcParams p)
                 // nearly always every row sees the whole tile
                 const uint4 readable = *reinterpret_cast<const uint4 *>(sm.seen[g & 3]);
                 full = full && (readable.x & readable.y & readable.z & readable.w) == ~0u;
-                auto visible = [&](int c) {  // of the tile's columns 32 c ..
-                    const int below = row_hi - 32 * c, from = (int)((uint32_t)below - (uint32_t)p.width);
-                    const uint32_t a = below >= 32 ? ~0u : (below <= 0 ? 0u : (1u << below) - 1u);
-                    const uint32_t z = from <= 0 ? 0u : (from >= 32 ? ~0u : (1u << from) - 1u);
-                    return a & ~z & sm.seen[g & 3][c];
-                };
                 uint32_t x0[32], x1[32];
+                if (!full) {
+                    // -inf for keys that a row does not see (in tensor memory, so that the
+                    // code below, that most tiles take, is short)
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        const int below = row_hi - 32 * c, from = (int)((uint32_t)below - (uint32_t)p.width);
+                        const uint32_t a = below >= 32 ? ~0u : (below <= 0 ? 0u : (1u << below) - 1u);
+                        const uint32_t z = from <= 0 ? 0u : (from >= 32 ? ~0u : (1u << from) - 1u);
+                        const uint32_t vis = a & ~z & sm.seen[g & 3][c];
+                        tm_load32(s_at + 32 * c, x1);
+                        tm_wait_ld(x1);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (!(vis & (1u << k))) x1[k] = 0xFF800000u;
+                        tm_store32(s_at + 32 * c, x1);
+                    }
+                    tm_wait_st();
+                }
                 auto top_of = [&](int c0, int c1) {  // the largest score of columns 32 c0 .. (in x1)
                     float top = kNoMax;
 #pragma unroll 1
                     for (int c = c0; c < c1; ++c) {
                         tm_load32(s_at + 32 * c, x1);
                         tm_wait_ld(x1);
-                        if (!full) {
-                            const uint32_t vis = visible(c);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!(vis & (1u << k))) x1[k] = 0xFF800000u;
-                        }
                         float a[4] = {top, kNoMax, kNoMax, kNoMax};
 #pragma unroll
                         for (int k = 0; k < 32; ++k) a[k & 3] = fmaxf(a[k & 3], __uint_as_float(x1[k]) * scale);
@@ -704,12 +847,6 @@ paged_attn_tc_kernel(const TcParams p)
                     sum[0] = sum[1] = sum[2] = sum[3] = 0.0f;
                     const float2 s2 = make_float2(scale, scale), nm = make_float2(-m, -m);
                     auto exps = [&](uint32_t (&x)[32], int c) {  // one chunk of P and of the sum
-                        if (!full) {
-                            const uint32_t vis = visible(c);
-#pragma unroll
-                            for (int k = 0; k < 32; ++k)
-                                if (!(vis & (1u << k))) x[k] = 0xFF800000u;  // -inf
-                        }
                         // 16 at a time: the exponentials first, then what uses them
                         // (this file is compiled with little instruction scheduling,
                         // so that they stay apart: the scheduler's own order put each
@@ -770,6 +907,19 @@ paged_attn_tc_kernel(const TcParams p)
                 if (lane == 0) bar_arrive(bars.p_full + 8 * t);
             }
             // ------------------------------------------------------ last step
+            bool store = !SHARE || w.parts == 1;
+            if (SHARE && w.parts > 1) {
+                if (!warp_wait(bars.pv_done + 8 * t, (end - 1) & 1, failed)) l = __uint_as_float(0x7FC00000u);
+                tm_fence_after();
+                const int mine = w.slot % w.parts;
+                const Joined j = share_part<DT>(
+                    p.workspace + kTakenBytes + p.parts_at + (w.slot - mine) * kSharedPartBytes,
+                    reinterpret_cast<unsigned *>(p.workspace) + 4 + w.shared * 8 + warp, mine, w.parts, t * kTile + r,
+                    o_at, tile, r, m, l, sm.v_gs);
+                m = j.m;
+                l = j.l;
+                store = j.last;
+            }
             // the next block's queries on their way meanwhile
             const bool told = warp_wait(bars.work_full + 8 * ((i + 1) & 1), ((i + 1) >> 1) & 1, failed);
             more = told && sm.work[(i + 1) & 1].rows > 0;
@@ -781,31 +931,18 @@ paged_attn_tc_kernel(const TcParams p)
             // through the tile's place of Q, so that a row's 256 bytes leave together
             const bool bad = *failed;
             const float inv = bad ? __uint_as_float(0x7FC00000u) : out_factor(l, sm.v_gs);
-            const bool none = l == 0.0f && !bad;
-            auto put_out = [&](uint32_t (&y)[32], int c) {
+            if (!SHARE || w.parts == 1) {
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    float e[8];
-#pragma unroll
-                    for (int n = 0; n < 8; ++n) e[n] = none ? 0.0f : __uint_as_float(y[k + n]) * inv;
-                    const uint4 v = pack8<DT>(e);
-                    const int chunk = 4 * c + k / 8;
-                    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};"
-                                 :: "r"(tile + (chunk >> 3) * (kTileBytes / 2) + r * 128 +
-                                        (((chunk & 7) ^ (r & 7)) << 4)),
-                                    "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t y[32];  // (of no meaning without keys: inv is 0 then)
+                    tm_load32(o_at + 32 * c, y);
+                    tm_wait_ld(y);
+                    put_out<DT>(tile, r, c, y, inv);
                 }
-            };
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t y[32];  // (of no meaning without keys: none is true then)
-                tm_load32(o_at + 32 * c, y);
-                tm_wait_ld(y);
-                put_out(y, c);
             }
             __syncwarp();
             const int row = w.row0 + t * kTile + r, query = row / p.per;
-            const bool real = t * kTile + r < w.rows;
+            const bool real = store && t * kTile + r < w.rows;
             const int out_row = (w.q0 + query) * p.hq + w.head * p.per + row - query * p.per;
 #pragma unroll
             for (int n0 = 0; n0 < 16; n0 += 4) {
@@ -840,35 +977,49 @@ paged_attn_tc_kernel(const TcParams p)
     }
 }
 
-}  // namespace
-
-template <typename DT>
-cudaError_t launch_paged_attn_tc(const PagedAttnParams &p, cudaStream_t stream)
+template <typename DT, bool SHARE>
+cudaError_t launch(const TcParams &p, int dev, unsigned ctas, cudaStream_t stream)
 {
     static std::atomic<int> ready[64];
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    auto kern = paged_attn_tc_kernel<DT>;
+    auto kern = paged_attn_tc_kernel<DT, SHARE>;
     if (dev >= 64 || !ready[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready[dev].store(1, std::memory_order_relaxed);
     }
+    return launch_pdl(kern, ctas, kThreads, kSmemBytes, stream, p);
+}
+
+}  // namespace
+
+template <typename DT>
+cudaError_t launch_paged_attn_tc(const PagedAttnParams &p, size_t parts_at, cudaStream_t stream)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
     // every sequence has a part of a row block at most beside its full ones
     const int64_t rows = p.n_tokens * p.per;
-    const int64_t blocks = rows / kRows + (rows / (p.few + 1) < p.n_seqs ? rows / (p.few + 1) : p.n_seqs);
-    if (blocks * p.hk > INT32_MAX) return cudaErrorInvalidConfiguration;
+    const int64_t blocks = (rows / kRows + (rows / (p.few + 1) < p.n_seqs ? rows / (p.few + 1) : p.n_seqs)) * p.hk;
+    if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
     if (blocks == 0) return cudaSuccess;
     TcParams tp;
     static_cast<PagedAttnParams &>(tp) = p;
-    tp.limit = (unsigned)(blocks * p.hk);
+    tp.limit = (unsigned)blocks;
     tp.width = p.window > 0 ? p.window : 1 << 30;
-    const unsigned sms = (unsigned)device_sms(dev);
-    return launch_pdl(kern, tp.limit < sms ? tp.limit : sms, kThreads, kSmemBytes, stream, tp);
+    tp.parts_at = parts_at;
+    // Few waves of blocks with many keys: those left over from whole waves are
+    // shared out by keys.  2 chunks of 2047 tokens after 14 thousand, 3.4 waves: 662
+    // us (710 without); 8 prompts of 1024, 3.4 waves of few keys, 57 us (55) and 5
+    // waves in a window of 2048 keys 181 us (178): the longer kernel misses its
+    // instruction cache more often.
+    const int64_t sms = device_sms(dev);
+    if (blocks <= 4 * sms && p.max_keys >= 2 * kPartTiles * kTile)
+        return launch<DT, true>(tp, dev, (unsigned)(8 * blocks < sms ? 8 * blocks : sms), stream);
+    return launch<DT, false>(tp, dev, (unsigned)(blocks < sms ? blocks : sms), stream);
 }
 
-template cudaError_t launch_paged_attn_tc<BF16>(const PagedAttnParams &, cudaStream_t);
-template cudaError_t launch_paged_attn_tc<FP16>(const PagedAttnParams &, cudaStream_t);
+template cudaError_t launch_paged_attn_tc<BF16>(const PagedAttnParams &, size_t, cudaStream_t);
+template cudaError_t launch_paged_attn_tc<FP16>(const PagedAttnParams &, size_t, cudaStream_t);
 
 }  // namespace rq
