@@ -25,16 +25,17 @@
 // operands of a 128 x 128 x 16 product are 8 KB of shared memory in its 64
 // clocks (4 KB with P in tensor memory), the decoded tile another 32 bytes a
 // clock, and the exponentials need half the time of the products.  A tile takes
-// about 2830 clocks where its products take 2048: S waits for the product with V
-// and its own (1330 clocks with the signals), P for the softmax (1500).  With
-// neither exponentials nor decoding it still takes 2500.  8192 tokens of 32 + 8
-// heads: 382 us, 1440 TFLOP/s.
+// about 2900 clocks where its products take 2048: S waits 1350 for the product
+// with V, its own and the signals, P 1550 for the softmax.  Without exponentials
+// and decoding it still took 2500.  8192 tokens of 32 + 8 heads: 380 us, 1445
+// TFLOP/s.
 //
-// A block begins and ends in about 9000 clocks (queries 2500, first maximum 400,
-// output 4500); one CTA a block, with its own start, took 12,000 more (8 prompts of
-// 1024 tokens 58 us, 55 like this).  Instruction caches are short for so much
-// straight code: code that few tiles need is kept out of the loop over the keys
-// (with the masks inline a tile took 3100 clocks).
+// From a block's last P to the next block's first scores it is 9000 clocks (last
+// product 2200, output 4000, queries into the tiles 1800, product 1000), from a
+// CTA's start 12,000 to 15,000: one CTA a block took that each time (8 prompts of
+// 1024 tokens 58 us, 55 like this).  The code is long for the instruction caches:
+// what few tiles need is kept out of the loop over the keys (with the masks inline
+// 8192 tokens took 417 us).
 //
 // Every wait has a time limit (kWaitNs): past it the CTA gives up, writes NaN
 // for its block and leaves, tensor memory freed.  No valid call meets it.

@@ -448,6 +448,39 @@ def test_repeatable_and_graph_replay():
         assert all(torch.equal(o.view(torch.int16), want.view(torch.int16)) for o in outs[i])
 
 
+@pytest.mark.parametrize("lens, new, hq, hk", [([9600, 40], [600, 40], 8, 1), ([1000, 0, 1500, 700], [1000, 50, 700, 700], 32, 4),
+                                               ([2500, 1], [900, 1], 16, 2)])
+def test_extend_repeats_streams_and_replays(lens, new, hq, hk):
+    """The same bits from calls one after another on one workspace, from two streams
+    at once, and from a captured call replayed between others on its stream."""
+    c = Cache(39, lens, hk, 32)
+    starts = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    q = [dev16(synth.normal_tensor(i, 4, (sum(new), hq, D), "bf16"), "bf16") for i in range(2)]
+    one, two = f32dev(GS_K), f32dev(GS_V)
+    call = lambda x, **kw: rq.paged_extend_attn_nvfp4(x, c.dpool, 32, c.dtable, starts, c.dlens, max(new), one, two,  # noqa: E731
+                                                      0.09, **kw)[0].view(torch.int16)
+    want = [call(x) for x in q]
+    ws = [torch.full((rq.rq_paged_attn_nvfp4_workspace_bytes(hq, hk),), 0xFF, dtype=torch.uint8, device="cuda")
+          for _ in range(2)]
+    for i in range(20):
+        assert torch.equal(call(q[i % 2], workspace=ws[0]), want[i % 2])
+    s = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [(i, call(q[i], workspace=ws[i], stream=s[i])) for _ in range(10) for i in range(2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i]) for i, o in outs)
+    x = q[0].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = call(x, workspace=ws[0])
+    for i in (0, 1, 1, 0):
+        x.copy_(q[i])
+        g.replay()
+        other = call(q[1 - i], workspace=ws[0])
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[i]) and torch.equal(other, want[1 - i])
+
+
 def test_far_pages():
     """Pages more than 4 GB into the cache."""
     c = Cache(16, [150, 90], 2, 64)
