@@ -447,11 +447,14 @@ def _same_device(tensors):
     """The index of the device that every given tensor lies on."""
     dev = tensors[0].get_device()
     for t in tensors:
-        if t is not None and t.get_device() != dev or dev < 0:
-            bad = tensors[0] if dev < 0 else t
-            raise ValueError("every tensor argument must be a CUDA tensor on one device (got %s and %s)"
-                             % (tensors[0].device, bad.device))
-    return dev
+        if t is not None and t.get_device() != dev:
+            break
+    else:
+        if dev >= 0:
+            return dev
+        t = tensors[0]
+    raise ValueError("every tensor argument must be a CUDA tensor on one device (got %s and %s)"
+                     % (tensors[0].device, t.device))
 
 
 def _call_on(dev, fn, args, stream):
@@ -506,8 +509,15 @@ def rq_qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos
     (include/rq.h).  q [T, Hq, 128], k, v [T, Hk, 128] may be token-strided
     views; q_out [T, Hq, 128]; kv_pool uint8 [pages, Hk, page_size * 144];
     slots int64 [T] (page * page_size + index; outside the cache: not stored)."""
+    _append(q, k, v, q_weight, k_weight, eps, positions, cos_sin_cache, k_global_scale, v_global_scale,
+            q_out, kv_pool, slots, page_size, stream, False)
+
+
+def _append(q, k, v, q_weight, k_weight, eps, positions, cos_sin_cache, k_global_scale, v_global_scale,
+            q_out, kv_pool, slots, page_size, stream, made):
+    # made: q_out was allocated here for q, and needs no check
     dev = _same_device((q, k, v, q_weight, k_weight, positions, cos_sin_cache, k_global_scale,
-                        v_global_scale, q_out, kv_pool, slots))
+                        v_global_scale, kv_pool, slots, None if made else q_out))
     qp, qs = _head_rows(q, "q")
     kp, ks = _head_rows(k, "k", q)
     vp, vs = _head_rows(v, "v", q)
@@ -528,13 +538,16 @@ def rq_qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos
         qp, kp, vp, qs, ks, vs, t, hq, hk, d, None if q_weight is None else q_weight.data_ptr(),
         None if k_weight is None else k_weight.data_ptr(), eps, _typed(positions, _I32, t, "positions"),
         cos_sin_cache.data_ptr(), table[0], _typed(k_global_scale, _F32, 1, "k_global_scale"),
-        _typed(v_global_scale, _F32, 1, "v_global_scale"), _typed(q_out, dtype, t * hq * d, "q_out"),
+        _typed(v_global_scale, _F32, 1, "v_global_scale"),
+        q_out.data_ptr() if made else _typed(q_out, dtype, t * hq * d, "q_out"),
         pool, pages, page, _typed(slots, _I64, t, "slots"), _dt(q)), stream)
 
 
 def _paged_attn(q, kv_pool, page_size, block_table, q_starts, max_q_len, kv_lens, k_gs, v_gs,
-                sm_scale, out, workspace, window, lse, stream):
-    dev = _same_device((q, kv_pool, block_table, q_starts, kv_lens, k_gs, v_gs, out, workspace, lse))
+                sm_scale, out, workspace, window, lse, stream, made=False):
+    # made: out and lse were allocated here for q, and need no check
+    dev = _same_device((q, kv_pool, block_table, q_starts, kv_lens, k_gs, v_gs, workspace) if made else
+                       (q, kv_pool, block_table, q_starts, kv_lens, k_gs, v_gs, workspace, out, lse))
     qp, qs = _head_rows(q, "q")
     t, hq, d = q.shape
     hk = kv_pool.shape[1] if kv_pool.dim() == 3 else 0
@@ -552,8 +565,9 @@ def _paged_attn(q, kv_pool, page_size, block_table, q_starts, max_q_len, kv_lens
     if workspace is None or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor")
     tail = (_typed(kv_lens, _I32, n, "kv_lens"), sm_scale, window, _typed(k_gs, _F32, 1, "k_global_scale"),
-            _typed(v_gs, _F32, 1, "v_global_scale"), _typed(out, q.dtype, t * hq * d, "out"),
-            None if lse is None else _typed(lse, _F32, t * hq, "lse"), workspace.data_ptr(),
+            _typed(v_gs, _F32, 1, "v_global_scale"),
+            out.data_ptr() if made else _typed(out, q.dtype, t * hq * d, "out"),
+            None if lse is None else lse.data_ptr() if made else _typed(lse, _F32, t * hq, "lse"), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), _dt(q))
     if q_starts is None:
         if t != n:
@@ -699,9 +713,8 @@ def qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos_si
     else:
         with _on_stream(stream, q.device):
             q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
-    rq_qkv_rope_nvfp4_kv_append(q, k, v, q_weight, k_weight, eps, positions, cos_sin_cache,
-                                k_global_scale, v_global_scale, q_out, kv_pool, slots, page_size,
-                                stream)
+    _append(q, k, v, q_weight, k_weight, eps, positions, cos_sin_cache, k_global_scale, v_global_scale,
+            q_out, kv_pool, slots, page_size, stream, True)
     return q_out
 
 
@@ -725,7 +738,7 @@ def paged_decode_attn_nvfp4(q, kv_pool, page_size, block_table, kv_lens, k_globa
     rq_paged_decode_attn_nvfp4.  Returns (out, lse or None)."""
     out, lse, workspace = _attn_buffers(q, kv_pool, with_lse, workspace, stream)
     _paged_attn(q, kv_pool, page_size, block_table, None, 1, kv_lens, k_global_scale,
-                v_global_scale, sm_scale, out, workspace, window, lse, stream)
+                v_global_scale, sm_scale, out, workspace, window, lse, stream, True)
     return out, lse
 
 
@@ -739,5 +752,5 @@ def paged_extend_attn_nvfp4(q, kv_pool, page_size, block_table, q_starts, kv_len
         raise ValueError("q_starts must be an int32 [n_seqs + 1] tensor")
     out, lse, workspace = _attn_buffers(q, kv_pool, with_lse, workspace, stream)
     _paged_attn(q, kv_pool, page_size, block_table, q_starts, max_q_len, kv_lens, k_global_scale,
-                v_global_scale, sm_scale, out, workspace, window, lse, stream)
+                v_global_scale, sm_scale, out, workspace, window, lse, stream, True)
     return out, lse
