@@ -846,6 +846,28 @@ bool is_short(const PagedAttnParams &p, int dev)
     return (int64_t)p.n_seqs * p.hk * kCluster <= (NT == 1 ? 4 : 1) * device_sms(dev) && p.max_keys <= 16384;
 }
 
+// Whether the tensor-memory kernel is faster for the runs of queries.  Both
+// kernels' times go with the keys: here a block of 16 columns takes 35 ps a key,
+// spread over every SM, there one of 256 rows 11.7 ns on one SM or, where blocks are
+// few, on up to 8 (the join 3 us a part).  Measured (here, there) in us: 4
+// sequences of 30,000 keys, 2 KV heads and 48, 128, 256 and 512 columns 42, 82, 148
+// and 280 (91, 90, 80 and 81), 8 heads 116, 281, 542 and 1066 (147, 141, 129 and
+// 217); 16 of 1000 keys and 8 heads 37, 73, 132 and 248 (28, 28, 27 and 46); 1 of
+// 4000 and 2 heads 19, 19, 21 and 25 (before parts of few tiles 60 to 71).  The keys
+// are the table's room, up to 8192: most sequences do not fill a wider one.
+bool runs_pay(const PagedAttnParams &p, int sms)
+{
+    const int64_t rows = (int64_t)p.per * p.n_tokens;
+    double keys = p.max_keys < 8192 ? p.max_keys : 8192;
+    if (p.window > 0 && keys > p.window + p.max_q) keys = p.window + p.max_q;
+    const double blocks16 = (double)(rows / 16 + p.n_seqs) * p.hk, blocks = (double)(rows / 256 + p.n_seqs) * p.hk;
+    double parts = kSharedBlocks / blocks < 8 ? kSharedBlocks / blocks : 8;
+    if (parts > keys / 1024) parts = keys / 1024;
+    const double waves = blocks > sms ? blocks / sms : 1;
+    const double there = parts >= 2 ? 15 + 0.0117 * keys / parts + 3 * parts : 15 + 0.0117 * keys * waves;
+    return there < 14 + 3.5e-5 * blocks16 * keys;
+}
+
 }  // namespace
 
 size_t paged_attn_workspace_bytes(int, int)
@@ -866,16 +888,7 @@ cudaError_t launch_paged_attn(const PagedAttnParams &p, cudaStream_t stream)
     few.few = INT_MAX;
     if (cols <= 8)
         return is_short<1>(few, dev) ? launch_cluster<DT, 1>(few, dev, stream) : launch_split<DT, 1>(few, dev, stream);
-    // This kernel's time goes with blocks of 16 columns, spread over every SM;
-    // the tensor-memory kernel's with waves of 256-row blocks, each on one SM for
-    // all its keys.  Measured at 8 KV heads, 16-column blocks here against
-    // waves there: 1 sequence of 30,000 keys and 128, 256 and 512 columns 106,
-    // 197 and 381 us (396, 354 and 355 there); 4 of 8192 and 64, 128 and 256
-    // 66, 119 and 223 (125, 119 and 108); 32 of 2048 and 36, 48 and 64 88,
-    // 103 and 132 (81, 83 and 80): equal near 270 blocks a wave.
-    const int64_t rows = (int64_t)p.per * p.n_tokens, sms = device_sms(dev);
-    const int64_t blocks16 = (rows / 16 + p.n_seqs) * p.hk, blocks256 = (rows / 256 + p.n_seqs) * p.hk;
-    if (p.q_starts == nullptr || cols <= kFewColumns || blocks16 <= 270 * ((blocks256 + sms - 1) / sms))
+    if (p.q_starts == nullptr || cols <= kFewColumns || !runs_pay(p, device_sms(dev)))
         return cols <= 16 && is_short<2>(few, dev) ? launch_cluster<DT, 2>(few, dev, stream)
                                                 : launch_split<DT, 2>(few, dev, stream);
     few.few = kFewColumns;

@@ -67,7 +67,7 @@ struct TcParams : PagedAttnParams {
 // of them see, in n tiles from lo; or one of the parts of a block whose keys
 // several CTAs share (parts 0: the others have it all).
 struct Work {
-    int seq, head, q0, first_pos, row0, rows, lo, first, hi, n, parts, shared, slot;
+    int seq, head, q0, first_pos, row0, rows, lo, first, hi, n, parts, part, shared, slot;
 };
 
 struct Small {
@@ -461,15 +461,16 @@ paged_attn_tc_kernel(const TcParams p)
         w.n = w.hi > w.lo ? (w.hi - w.lo + kTile - 1) / kTile : 0;
         w.parts = 1;
         if (SHARE && id >= whole && parts > 1) {
-            const int part = (id - whole) % parts, n = w.n;
-            if (n >= kPartTiles * (int)parts) {
-                w.lo += n * part / (int)parts * kTile;
-                w.n = n * (part + 1) / (int)parts - n * part / (int)parts;
-                w.parts = parts;
-                w.shared = (id - whole) / parts;
-                w.slot = id - whole;
-            } else if (part > 0) {
+            const int part = (id - whole) % parts, n = w.n, of = max(1, min((int)parts, n / kPartTiles));
+            if (part >= of) {
                 w.n = w.parts = 0;
+            } else if (of > 1) {
+                w.lo += n * part / of * kTile;
+                w.n = n * (part + 1) / of - n * part / of;
+                w.parts = of;
+                w.part = part;
+                w.shared = (id - whole) / parts;
+                w.slot = w.shared * parts;  // of the first part
             }
         }
     };
@@ -912,11 +913,10 @@ paged_attn_tc_kernel(const TcParams p)
             if (SHARE && w.parts > 1) {
                 if (!warp_wait(bars.pv_done + 8 * t, (end - 1) & 1, failed)) l = __uint_as_float(0x7FC00000u);
                 tm_fence_after();
-                const int mine = w.slot % w.parts;
                 const Joined j = share_part<DT>(
-                    p.workspace + kTakenBytes + p.parts_at + (w.slot - mine) * kSharedPartBytes,
-                    reinterpret_cast<unsigned *>(p.workspace) + 4 + w.shared * 8 + warp, mine, w.parts, t * kTile + r,
-                    o_at, tile, r, m, l, sm.v_gs);
+                    p.workspace + kTakenBytes + p.parts_at + w.slot * kSharedPartBytes,
+                    reinterpret_cast<unsigned *>(p.workspace) + 4 + w.shared * 8 + warp, w.part, w.parts,
+                    t * kTile + r, o_at, tile, r, m, l, sm.v_gs);
                 m = j.m;
                 l = j.l;
                 store = j.last;
