@@ -848,13 +848,14 @@ bool is_short(const PagedAttnParams &p, int dev)
 
 // Whether the tensor-memory kernel is faster for the runs of queries.  Both
 // kernels' times go with the keys: here a block of 16 columns takes 35 ps a key,
-// spread over every SM, there one of 256 rows 11.7 ns on one SM or, where blocks are
-// few, on up to 8 (the join 3 us a part).  Measured (here, there) in us: 4
+// spread over every SM, there one of 256 rows 11.7 ns on one SM or, where blocks
+// are few, on up to 8 (the join 3 us a part).  Measured (here, there) in us: 4
 // sequences of 30,000 keys, 2 KV heads and 48, 128, 256 and 512 columns 42, 82, 148
-// and 280 (91, 90, 80 and 81), 8 heads 116, 281, 542 and 1066 (147, 141, 129 and
-// 217); 16 of 1000 keys and 8 heads 37, 73, 132 and 248 (28, 28, 27 and 46); 1 of
-// 4000 and 2 heads 19, 19, 21 and 25 (before parts of few tiles 60 to 71).  The keys
-// are the table's room, up to 8192: most sequences do not fill a wider one.
+// and 280 (91, 90, 80 and 81), 8 heads and 48, 128, 256 and 512 116, 281, 542 and
+// 1066 (147, 141, 129 and 217); 16 of 1000 keys, 8 heads and the same 37, 73, 132
+// and 248 (28, 28, 27 and 46); 1 of 4000 keys, 8 heads and 512 columns 58 (41).
+// The keys are the table's room, up to 8192: most sequences do not fill a wider
+// one.
 bool runs_pay(const PagedAttnParams &p, int sms)
 {
     const int64_t rows = (int64_t)p.per * p.n_tokens;

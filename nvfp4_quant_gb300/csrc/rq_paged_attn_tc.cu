@@ -27,7 +27,7 @@
 // clock, and the exponentials need half the time of the products.  A tile takes
 // about 2900 clocks where its products take 2048: S waits 1350 for the product
 // with V, its own and the signals, P 1550 for the softmax.  Without exponentials
-// and decoding it still took 2500.  8192 tokens of 32 + 8 heads: 380 us, 1445
+// and decoding it still took 2500.  8192 tokens of 32 + 8 heads: 376 us, 1460
 // TFLOP/s.
 //
 // From a block's last P to the next block's first scores it is 9000 clocks (last
