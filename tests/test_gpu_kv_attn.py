@@ -352,6 +352,14 @@ def test_extend_long_chunk():
     run_extend(Cache(11, [2500, 600], 2, 16), 4, [700, 600], "fp16", window=600)
 
 
+@pytest.mark.parametrize("window", [0, 200])
+def test_extend_wide_table(window):
+    """Room for 20,000 keys, few of them there: parts of blocks that have nothing to do."""
+    c = Cache(40, [500, 90, 1300, 3000, 4], 2, 32, stride_extra=600)
+    run_extend(c, 16, [400, 90, 700, 50, 4], "bf16", window=window, behind=2)
+    run_extend(c, 32, [400, 90, 700, 900, 4], "fp16", window=window)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 def test_extend_more_blocks_than_sms(dt):
     """Blocks after one another on an SM, many of them without a key."""
